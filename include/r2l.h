@@ -89,6 +89,8 @@ typedef enum {
 #define R2L_FLAG_SAVED_FORWARD 0x4u /* r2l_sidecar_backward only: the workspace holds this hook's
                                        forward from r2l_sidecar_forward_train, so the forward is
                                        not recomputed                                             */
+#define R2L_FLAG_ACT8 0x8u          /* r2l_gated_scan_train and its gradient only: the checkpoint also
+                                       keeps x, r and g, in 8 bits (see r2l_act8_pack)            */
 /* Device status bits, reported by r2l_get_device_status(). */
 #define R2L_DEVFLAG_LENGTH_CLAMPED 0x1u   /* a lengths[b] was outside [0, L] and was clamped */
 #define R2L_DEVFLAG_TIMEOUT 0x2u          /* a kernel gave up waiting on a pipeline barrier (results invalid) */
@@ -366,6 +368,125 @@ R2L_API r2l_status r2l_sidecar_backward(const void *hidden, const r2l_weights *w
 R2L_API r2l_status r2l_sidecar_forward_train(const void *hidden, void *out, const r2l_weights *weights,
                                              const r2l_dims *dims, float s, int B, int L, const int32_t *lengths,
                                              void *workspace, size_t workspace_bytes, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * A gated linear recurrence: one state per channel, whose decay and input are
+ * gated position by position by two projections of the layer's input.  For an
+ * input x, a recurrence gate r and an input gate g (all before the sigmoid) and
+ * a decay parameter lam per channel, at position k of the scan order,
+ *
+ *     log a_k = -R2L_GATED_RATE · softplus(lam) · σ(r_k)
+ *     h_k     = a_k ⊙ h_{k-1} + sqrt(1 − a_k²) ⊙ σ(g_k) ⊙ x_k,      y_k = h_k
+ *
+ * The scan runs from each sequence's last valid position to its first, as
+ * r2l_reverse_scan does, or the other way with R2L_FLAG_FORWARD_SCAN.  A state
+ * may enter (h0) and leave (h_last), so a sequence can be scanned in pieces, a
+ * piece of one position being one step of decoding.  r = −∞ closes the
+ * recurrence gate: a_k = 1, and the position leaves the state as it was.
+ * State, gates and sums are fp32 for both dtypes.
+ *
+ * r2l_dims: d_inner is the number of channels E (any positive number), dtype
+ * the type of the [B·L, ·] arrays, flags R2L_FLAG_FORWARD_SCAN and
+ * R2L_FLAG_ACT8; the other fields are not read.
+ *
+ * Arrays of rows have a row stride (ld…) in elements, at least E, so that they
+ * can be columns of a wider array; row b·L + i is position i of sequence b.
+ * Pointers need the alignment of their element type only; a call whose arrays
+ * of rows all start on 16-byte boundaries with strides that are multiples of
+ * 16 bytes runs faster.  No output may overlap an input, except h_last = h0
+ * and dh0 = dh_last.  lengths as for r2l_sidecar_forward (clamped to [0, L];
+ * a sequence of length 0 passes its state through).
+ * ------------------------------------------------------------------------- */
+#define R2L_GATED_RATE 8.0f
+#define R2L_GATED_TILE 64   /* positions between two states of a checkpoint */
+
+typedef struct {
+  const void *x;      /* act  [B·L, ldx]                                        */
+  const void *r;      /* act  [B·L, ldr]  recurrence gate, before the sigmoid   */
+  const void *g;      /* act  [B·L, ldg]  input gate, before the sigmoid        */
+  int ldx, ldr, ldg;
+  const float *lam;   /* fp32 [E]                                               */
+  const float *h0;    /* fp32 [B, E] state that enters the scan, NULL: 0        */
+} r2l_gated_in;
+
+typedef struct {
+  void *dx, *dr, *dg;           /* act [B·L, ld…]; rows i ≥ len_b are written with zeros  */
+  int ld_dx, ld_dr, ld_dg;
+  float *dlam;                  /* fp32 [E], summed over the batch                        */
+  float *dh0;                   /* fp32 [B, E], or NULL: not wanted                       */
+} r2l_gated_grads;
+
+/* The recurrence.  y: act [B·L, ldy], rows i ≥ len_b are not written.  h_last:
+ * fp32 [B, E], the state that leaves the scan, or NULL; it may be in->h0.
+ * status: device word that receives the R2L_DEVFLAG_* bits of this call (what
+ * r2l_get_device_status reads), or NULL.  No workspace is needed, and nothing
+ * is enqueued on an error.  The result does not depend on the other sequences
+ * of the batch or on B; it is bitwise reproducible for given B, L and E.     */
+R2L_API r2l_status r2l_gated_scan(const r2l_gated_in *in, void *y, int ldy, float *h_last, const r2l_dims *dims,
+                                  int B, int L, const int32_t *lengths, uint32_t *status, void *stream);
+
+/* Bytes of the checkpoint that r2l_gated_scan_train writes; 0 for invalid
+ * input.  Without R2L_FLAG_ACT8 it holds the state that enters every
+ * R2L_GATED_TILE-th position of the scan order (fp32, 1/16 of a value per
+ * position and channel); with it also x, r and g as r2l_act8_pack packs them
+ * (3 + 3/64 bytes per position and channel).                                 */
+R2L_API size_t r2l_gated_scan_checkpoint_size(const r2l_dims *dims, int B, int L);
+
+/* r2l_gated_scan for training: also writes `checkpoint`
+ * (≥ r2l_gated_scan_checkpoint_size(dims, B, L) bytes, 16-byte aligned,
+ * caller-owned), which r2l_gated_scan_backward reads.                        */
+R2L_API r2l_status r2l_gated_scan_train(const r2l_gated_in *in, void *y, int ldy, float *h_last, const r2l_dims *dims,
+                                        int B, int L, const int32_t *lengths, void *checkpoint,
+                                        size_t checkpoint_bytes, uint32_t *status, void *stream);
+
+/* Bytes of workspace of r2l_gated_scan_backward; 0 for invalid input. */
+R2L_API size_t r2l_gated_scan_backward_workspace_size(const r2l_dims *dims, int B, int L);
+
+/* Gradient of r2l_gated_scan.  For dy = ∂L/∂y (act [B·L, ld_dy]) and dh_last =
+ * ∂L/∂h_last (fp32 [B, E], NULL: 0), with G_k = ∂L/∂h_k = dy_k + a_{k+1} G_{k+1}
+ * and β = sqrt(1 − a²):
+ *
+ *   dx = G ⊙ β ⊙ σ(g)                    dg = G ⊙ β ⊙ x ⊙ σ(g)(1 − σ(g))
+ *   d(log a) = G ⊙ (a ⊙ h_{k-1} − σ(g) ⊙ x ⊙ a²/β)       (0 where log a = 0)
+ *   dr = d(log a) ⊙ log a ⊙ (1 − σ(r))   dlam = Σ d(log a) ⊙ σ(r) · (−R2L_GATED_RATE σ(lam))
+ *   dh0 = a_0 ⊙ G_0
+ *
+ * in: x, r, g and lam as given to the forward (h0 is not read: the checkpoint
+ * has it).  With R2L_FLAG_ACT8 x, r and g are not read either and may be NULL;
+ * the gradient is then the formula at the values that the checkpoint's 8 bits
+ * stand for, each tile's states recomputed from its exact first one.
+ * dims, B, L and lengths as given to r2l_gated_scan_train; dims->flags too.
+ * Every sum runs in a fixed order: results are bitwise reproducible.
+ * workspace ≥ r2l_gated_scan_backward_workspace_size(dims, B, L) bytes,
+ * 16-byte aligned; its first word is the device status word.                 */
+R2L_API r2l_status r2l_gated_scan_backward(const r2l_gated_in *in, const void *dy, int ld_dy, const float *dh_last,
+                                           const r2l_gated_grads *grads, const r2l_dims *dims, int B, int L,
+                                           const int32_t *lengths, const void *checkpoint, size_t checkpoint_bytes,
+                                           void *workspace, size_t workspace_bytes, void *stream);
+
+/* Activation checkpoints in 8 bits: what a training step keeps of an
+ * activation between its forward and its gradient (a hook's hidden state for
+ * r2l_sidecar_backward, which recomputes the hook's forward from it) in half
+ * the bytes of bf16.  A row is cut into groups of R2L_ACT8_GROUP channels (the
+ * last one may be shorter).  A group holds x / 2^k rounded to the nearest e4m3
+ * value, ties to even, and the byte k + 127, with k ≥ −126 the least integer
+ * for which every finite |x| of the group is ≤ 448 · 2^k.  The scale being a
+ * power of two, a value that e4m3's 4 significant bits hold comes back as it
+ * was, and packing what was unpacked changes nothing.  An infinity or a NaN
+ * comes back as NaN.                                                         */
+#define R2L_ACT8_GROUP 64
+
+/* Packs x (dtype, [B·L, ldx], its first `cols` columns) into q ([B·L, ldq]
+ * bytes, e4m3) and scales ([B·L, ⌈cols / R2L_ACT8_GROUP⌉] bytes).  lengths as
+ * for r2l_sidecar_forward (NULL: all rows); rows i ≥ len_b are neither read
+ * nor written.                                                               */
+R2L_API r2l_status r2l_act8_pack(const void *x, int ldx, r2l_dtype dtype, int B, int L, int cols,
+                                 const int32_t *lengths, uint8_t *q, int ldq, uint8_t *scales, void *stream);
+
+/* The values that q and scales stand for, into out (dtype, [B·L, ldo]),
+ * rounded to nearest where dtype needs it.  Arguments as r2l_act8_pack.      */
+R2L_API r2l_status r2l_act8_unpack(const uint8_t *q, int ldq, const uint8_t *scales, r2l_dtype dtype, int B, int L,
+                                   int cols, const int32_t *lengths, void *out, int ldo, void *stream);
 
 /* Synchronises `stream`, then reads the device status word that the last
  * forward call on `workspace` wrote.  *flags_out receives the R2L_DEVFLAG_*

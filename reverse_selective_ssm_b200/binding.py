@@ -20,6 +20,7 @@ R2L_BF16, R2L_FP32 = 0, 1
 R2L_FLAG_GENERAL_A = 0x1
 R2L_FLAG_FORWARD_SCAN = 0x2
 R2L_FLAG_SAVED_FORWARD = 0x4
+R2L_FLAG_ACT8 = 0x8
 R2L_DEVFLAG_LENGTH_CLAMPED = 0x1
 
 STATUS = {0: "R2L_OK", 1: "R2L_ERR_INVALID_ARG", 2: "R2L_ERR_UNSUPPORTED", 3: "R2L_ERR_ALIGNMENT",
@@ -30,9 +31,13 @@ EXPORTS = ("r2l_abi_version", "r2l_status_string", "r2l_workspace_size", "r2l_si
            "r2l_get_device_status", "r2l_reverse_scan_workspace_size", "r2l_reverse_scan",
            "r2l_reverse_scan_noalloc", "r2l_reverse_scan_backward_workspace_size",
            "r2l_reverse_scan_backward", "r2l_sidecar_backward_workspace_size", "r2l_sidecar_backward",
-           "r2l_sidecar_forward_train")
+           "r2l_sidecar_forward_train", "r2l_gated_scan", "r2l_gated_scan_checkpoint_size",
+           "r2l_gated_scan_train", "r2l_gated_scan_backward_workspace_size", "r2l_gated_scan_backward",
+           "r2l_act8_pack", "r2l_act8_unpack")
 
 NOALLOC_SCRATCH_BYTES = 16 << 20
+GATED_TILE = 64      # positions between two states of a gated scan's checkpoint
+ACT8_GROUP = 64      # channels that share a scale of an 8-bit activation checkpoint
 
 STAGES = ("in_proj", "conv", "x_proj", "dt_proj", "scan", "out_proj", "ln_residual")
 
@@ -61,6 +66,19 @@ class Grads(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in (
         "in_proj_w", "conv_w", "conv_b", "x_proj_w", "dt_proj_w", "dt_proj_b", "A_log", "D",
         "out_proj_w", "ln_w", "ln_b")]
+
+
+class GatedIn(ctypes.Structure):
+    """r2l_gated_in: x, r, g with their row strides, lam and h0."""
+    _fields_ = [("x", ctypes.c_void_p), ("r", ctypes.c_void_p), ("g", ctypes.c_void_p), ("ldx", ctypes.c_int),
+                ("ldr", ctypes.c_int), ("ldg", ctypes.c_int), ("lam", ctypes.c_void_p), ("h0", ctypes.c_void_p)]
+
+
+class GatedGrads(ctypes.Structure):
+    """r2l_gated_grads: dx, dr, dg with their row strides, dlam and dh0."""
+    _fields_ = [("dx", ctypes.c_void_p), ("dr", ctypes.c_void_p), ("dg", ctypes.c_void_p), ("ld_dx", ctypes.c_int),
+                ("ld_dr", ctypes.c_int), ("ld_dg", ctypes.c_int), ("dlam", ctypes.c_void_p),
+                ("dh0", ctypes.c_void_p)]
 
 
 class DebugOut(ctypes.Structure):
@@ -122,6 +140,22 @@ def load(path: str = LIB_PATH) -> ctypes.CDLL:
     lib.r2l_sidecar_forward_train.restype = ci
     lib.r2l_sidecar_forward_train.argtypes = [vp, vp, ctypes.POINTER(Weights), ctypes.POINTER(Dims), cf, ci, ci, vp,
                                               vp, ctypes.c_size_t, vp]
+    gin, dp, sz = ctypes.POINTER(GatedIn), ctypes.POINTER(Dims), ctypes.c_size_t
+    lib.r2l_gated_scan.restype = ci
+    lib.r2l_gated_scan.argtypes = [gin, vp, ci, vp, dp, ci, ci, vp, vp, vp]
+    lib.r2l_gated_scan_checkpoint_size.restype = sz
+    lib.r2l_gated_scan_checkpoint_size.argtypes = [dp, ci, ci]
+    lib.r2l_gated_scan_train.restype = ci
+    lib.r2l_gated_scan_train.argtypes = [gin, vp, ci, vp, dp, ci, ci, vp, vp, sz, vp, vp]
+    lib.r2l_gated_scan_backward_workspace_size.restype = sz
+    lib.r2l_gated_scan_backward_workspace_size.argtypes = [dp, ci, ci]
+    lib.r2l_gated_scan_backward.restype = ci
+    lib.r2l_gated_scan_backward.argtypes = [gin, vp, ci, vp, ctypes.POINTER(GatedGrads), dp, ci, ci, vp, vp, sz, vp,
+                                            sz, vp]
+    lib.r2l_act8_pack.restype = ci
+    lib.r2l_act8_pack.argtypes = [vp, ci, ci, ci, ci, ci, vp, vp, ci, vp, vp]
+    lib.r2l_act8_unpack.restype = ci
+    lib.r2l_act8_unpack.argtypes = [vp, ci, vp, ci, ci, ci, ci, vp, vp, ci, vp]
     lib.r2l_get_device_status.restype = ci
     lib.r2l_get_device_status.argtypes = [vp, vp, ctypes.POINTER(ctypes.c_uint32)]
     _LIB = lib
@@ -392,3 +426,231 @@ def sidecar_backward(hidden: torch.Tensor, weights, dims: Dims, s: float, dh_out
     if check and st != 0:
         raise R2LError(st, "r2l_sidecar_backward")
     return dh, ds[:1]
+
+
+# ---------------------------------------------------------------- gated linear recurrence
+
+_DTYPES = {R2L_BF16: torch.bfloat16, R2L_FP32: torch.float32}
+_CODES = {v: k for k, v in _DTYPES.items()}
+
+
+def gated_dims(channels: int, dtype: torch.dtype, flags: int = 0) -> Dims:
+    """Dims of a gated scan over ``channels`` channels (the other fields are not read)."""
+    return Dims(channels, channels, 16, 1, 4, _CODES[dtype], flags)
+
+
+class _On:
+    """Where a call runs: its tensors' device is made the current one, its stream the one its own tensors are
+    allocated on (torch then reuses their memory in that stream's order).  ``stream``: None for the device's
+    current stream, a torch stream or a raw cudaStream_t."""
+
+    def __init__(self, device: torch.device, stream):
+        self.guards = []
+        if device.index != torch.cuda.current_device():
+            self.guards.append(torch.cuda.device(device))
+        if stream is not None:
+            if not hasattr(stream, "cuda_stream"):
+                stream = torch.cuda.ExternalStream(int(stream), device=device)
+            self.guards.append(torch.cuda.stream(stream))
+        self.device, self.stream = device, stream
+
+    def __enter__(self) -> int:
+        for g in self.guards:
+            g.__enter__()
+        return (self.stream or torch.cuda.current_stream(self.device)).cuda_stream
+
+    def __exit__(self, *exc):
+        for g in reversed(self.guards):
+            g.__exit__(*exc)
+
+
+def _rows(t: torch.Tensor, M: int, E: int, dtype: torch.dtype, device: torch.device, name: str):
+    """(pointer, row stride) of [M, E] rows whose elements are contiguous: a tensor or columns of a wider one."""
+    if t.shape != (M, E):
+        raise ValueError(f"{name} must be [{M}, {E}], got {tuple(t.shape)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    row, col = t.stride()
+    if M == 1:
+        row = max(row, E)
+    if (col != 1 and E > 1) or row < E:
+        raise ValueError(f"{name}: rows must be contiguous and must not overlap (strides {(row, col)})")
+    return t.data_ptr(), row
+
+
+def _vec(t: Optional[torch.Tensor], shape, device: torch.device, name: str,
+         dtype: torch.dtype = torch.float32) -> Optional[int]:
+    """Pointer of a contiguous tensor of this shape and type (None: null)."""
+    if t is None:
+        return None
+    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous {dtype} {tuple(shape)} on {device}, got {t.dtype} "
+                         f"{tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _gated_inputs(x, r, g, lam, h0, dims, B, L):
+    if not x.is_cuda:
+        raise ValueError("libr2l takes device tensors")
+    E, dtype, dev = dims.d_inner, _DTYPES[dims.dtype], x.device
+    (px, ldx), (pr, ldr), (pg, ldg) = (_rows(t, B * L, E, dtype, dev, n) for t, n in ((x, "x"), (r, "r"), (g, "g")))
+    return GatedIn(px, pr, pg, ldx, ldr, ldg, _vec(lam, (E,), dev, "lam"), _vec(h0, (B, E), dev, "h0"))
+
+
+def _gated_forward(x, r, g, lam, dims, B, L, h0, lengths, checkpoint, y, h_last, status, stream, check, train):
+    lib = load()
+    gi = _gated_inputs(x, r, g, lam, h0, dims, B, L)
+    E, dev = dims.d_inner, x.device
+    with _On(dev, stream) as st:
+        if y is None:
+            y = torch.empty((B * L, E), dtype=x.dtype, device=dev)
+        if h_last is None:
+            h_last = torch.empty((B, E), dtype=torch.float32, device=dev)
+        py, ldy = _rows(y, B * L, E, x.dtype, dev, "y")
+        args = [ctypes.byref(gi), py, ldy, _vec(h_last, (B, E), dev, "h_last"), ctypes.byref(dims), B, L,
+                _vec(lengths, (B,), dev, "lengths", torch.int32)]
+        if train:
+            if checkpoint is None:
+                checkpoint = torch.empty(lib.r2l_gated_scan_checkpoint_size(ctypes.byref(dims), B, L),
+                                         dtype=torch.uint8, device=dev)
+            args += [_ptr(checkpoint), checkpoint.numel() * checkpoint.element_size()]
+        args += [None if status is None else _ptr(status), st]
+        rc = (lib.r2l_gated_scan_train if train else lib.r2l_gated_scan)(*args)
+    if check and rc != 0:
+        raise R2LError(rc, "r2l_gated_scan_train" if train else "r2l_gated_scan")
+    return y, h_last, checkpoint
+
+
+def gated_scan(x: torch.Tensor, r: torch.Tensor, g: torch.Tensor, lam: torch.Tensor, dims: Dims, B: int, L: int,
+               h0: Optional[torch.Tensor] = None, lengths: Optional[torch.Tensor] = None,
+               y: Optional[torch.Tensor] = None, h_last: Optional[torch.Tensor] = None,
+               status: Optional[torch.Tensor] = None, stream=None, check: bool = True):
+    """r2l_gated_scan: returns (y, h_last).  x, r, g, y: [B·L, E] rows of dims' dtype (columns of a wider tensor will
+    do); lam fp32 [E]; h0, h_last fp32 [B, E] (h_last may be h0); lengths int32 [B]; dims from :func:`gated_dims`.
+    Where y is allocated here, its rows past a sequence's length hold unspecified values."""
+    return _gated_forward(x, r, g, lam, dims, B, L, h0, lengths, None, y, h_last, status, stream, check, False)[:2]
+
+
+def gated_step(x: torch.Tensor, r: torch.Tensor, g: torch.Tensor, lam: torch.Tensor, dims: Dims, state: torch.Tensor,
+               new_state: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+               lengths: Optional[torch.Tensor] = None, stream=None, check: bool = True) -> torch.Tensor:
+    """One position of each of B sequences (x, r, g, y: [B, E]) on their states (fp32 [B, E]), which are updated in
+    place unless new_state is given: r2l_gated_scan with L = 1.  A sequence with lengths[b] = 0 keeps its state.
+    Returns y."""
+    return _gated_forward(x, r, g, lam, dims, state.shape[0], 1, state, lengths, None, y,
+                          state if new_state is None else new_state, None, stream, check, False)[0]
+
+
+def gated_scan_checkpoint_size(dims: Dims, B: int, L: int) -> int:
+    return int(load().r2l_gated_scan_checkpoint_size(ctypes.byref(dims), B, L))
+
+
+def gated_scan_train(x: torch.Tensor, r: torch.Tensor, g: torch.Tensor, lam: torch.Tensor, dims: Dims, B: int, L: int,
+                     h0: Optional[torch.Tensor] = None, lengths: Optional[torch.Tensor] = None,
+                     checkpoint: Optional[torch.Tensor] = None, y: Optional[torch.Tensor] = None,
+                     h_last: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None, stream=None,
+                     check: bool = True):
+    """r2l_gated_scan_train: returns (y, h_last, checkpoint); the checkpoint goes to :func:`gated_scan_backward`.
+    With R2L_FLAG_ACT8 in dims it also holds x, r and g in 8 bits, which the gradient then reads instead of them."""
+    return _gated_forward(x, r, g, lam, dims, B, L, h0, lengths, checkpoint, y, h_last, status, stream, check, True)
+
+
+def gated_scan_backward_workspace_size(dims: Dims, B: int, L: int) -> int:
+    return int(load().r2l_gated_scan_backward_workspace_size(ctypes.byref(dims), B, L))
+
+
+def gated_scan_backward(dy: torch.Tensor, lam: torch.Tensor, dims: Dims, B: int, L: int, checkpoint: torch.Tensor,
+                        x: Optional[torch.Tensor] = None, r: Optional[torch.Tensor] = None,
+                        g: Optional[torch.Tensor] = None, dh_last: Optional[torch.Tensor] = None,
+                        lengths: Optional[torch.Tensor] = None, dx: Optional[torch.Tensor] = None,
+                        dr: Optional[torch.Tensor] = None, dg: Optional[torch.Tensor] = None,
+                        workspace: Optional[torch.Tensor] = None, stream=None,
+                        check: bool = True) -> Dict[str, torch.Tensor]:
+    """r2l_gated_scan_backward: returns {"dx", "dr", "dg", "dlam", "dh0"} (dx, dr, dg in dims' dtype, [B·L, E],
+    allocated here unless given; dlam fp32 [E], dh0 fp32 [B, E]).  x, r and g as given to the forward; with
+    R2L_FLAG_ACT8 in dims they are not read and may be left out."""
+    lib = load()
+    if not dy.is_cuda:
+        raise ValueError("libr2l takes device tensors")
+    M, E, dtype, dev = B * L, dims.d_inner, _DTYPES[dims.dtype], dy.device
+    if dims.flags & R2L_FLAG_ACT8:
+        gi = GatedIn(None, None, None, 0, 0, 0, _vec(lam, (E,), dev, "lam"), None)
+    else:
+        if x is None or r is None or g is None:
+            raise ValueError("x, r and g are needed unless the checkpoint holds them (R2L_FLAG_ACT8)")
+        gi = _gated_inputs(x, r, g, lam, None, dims, B, L)
+    with _On(dev, stream) as st:
+        dx, dr, dg = (torch.empty((M, E), dtype=dtype, device=dev) if t is None else t for t in (dx, dr, dg))
+        out = {"dx": dx, "dr": dr, "dg": dg, "dlam": torch.empty(E, dtype=torch.float32, device=dev),
+               "dh0": torch.empty((B, E), dtype=torch.float32, device=dev)}
+        if workspace is None:
+            workspace = torch.empty(gated_scan_backward_workspace_size(dims, B, L), dtype=torch.uint8, device=dev)
+        (pdx, ldx), (pdr, ldr), (pdg, ldg) = (_rows(out[n], M, E, dtype, dev, n) for n in ("dx", "dr", "dg"))
+        gr = GatedGrads(pdx, pdr, pdg, ldx, ldr, ldg, out["dlam"].data_ptr(), out["dh0"].data_ptr())
+        pdy, ld_dy = _rows(dy, M, E, dtype, dev, "dy")
+        rc = lib.r2l_gated_scan_backward(ctypes.byref(gi), pdy, ld_dy, _vec(dh_last, (B, E), dev, "dh_last"),
+                                         ctypes.byref(gr), ctypes.byref(dims), B, L,
+                                         _vec(lengths, (B,), dev, "lengths", torch.int32), _ptr(checkpoint),
+                                         checkpoint.numel() * checkpoint.element_size(), _ptr(workspace),
+                                         workspace.numel() * workspace.element_size(), st)
+    if check and rc != 0:
+        raise R2LError(rc, "r2l_gated_scan_backward")
+    return out
+
+
+# ---------------------------------------------------------------- 8-bit activation checkpoints
+
+def act8_pack(x: torch.Tensor, B: int, L: int, lengths: Optional[torch.Tensor] = None,
+              q: Optional[torch.Tensor] = None, scales: Optional[torch.Tensor] = None, stream=None,
+              check: bool = True):
+    """r2l_act8_pack of x [B·L, cols] (bf16 or fp32; columns of a wider tensor will do): returns (q, scales), q
+    [B·L, cols] torch.float8_e4m3fn and scales [B·L, ⌈cols/64⌉] uint8.  Rows past a sequence's length are not written."""
+    lib = load()
+    if not x.is_cuda:
+        raise ValueError("libr2l takes device tensors")
+    if x.dim() != 2 or x.dtype not in _CODES:
+        raise ValueError("x must be [B·L, cols], bf16 or fp32")
+    M, cols, dev = B * L, x.shape[1], x.device
+    groups = -(-cols // ACT8_GROUP)
+    px, ldx = _rows(x, M, cols, x.dtype, dev, "x")
+    with _On(dev, stream) as st:
+        if q is None:
+            q = torch.empty((M, cols), dtype=torch.float8_e4m3fn, device=dev)
+        if scales is None:
+            scales = torch.empty((M, groups), dtype=torch.uint8, device=dev)
+        pq, ldq = _rows(q, M, cols, torch.float8_e4m3fn, dev, "q")
+        rc = lib.r2l_act8_pack(px, ldx, _CODES[x.dtype], B, L, cols, _vec(lengths, (B,), dev, "lengths", torch.int32),
+                               pq, ldq, _vec(scales, (M, groups), dev, "scales", torch.uint8), st)
+    if check and rc != 0:
+        raise R2LError(rc, "r2l_act8_pack")
+    return q, scales
+
+
+def act8_unpack(q: torch.Tensor, scales: torch.Tensor, B: int, L: int, dtype: torch.dtype = torch.bfloat16,
+                lengths: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None, stream=None,
+                check: bool = True) -> torch.Tensor:
+    """r2l_act8_unpack: the values that q and scales (from :func:`act8_pack`) stand for, [B·L, cols] in dtype (or in
+    out's).  Rows past a sequence's length are not written."""
+    lib = load()
+    if not q.is_cuda:
+        raise ValueError("libr2l takes device tensors")
+    if q.dim() != 2:
+        raise ValueError("q must be [B·L, cols]")
+    M, cols, dev = B * L, q.shape[1], q.device
+    if out is not None:
+        dtype = out.dtype
+    if dtype not in _CODES:
+        raise ValueError("the output is bf16 or fp32")
+    pq, ldq = _rows(q, M, cols, torch.float8_e4m3fn, dev, "q")
+    with _On(dev, stream) as st:
+        if out is None:
+            out = torch.empty((M, cols), dtype=dtype, device=dev)
+        po, ldo = _rows(out, M, cols, dtype, dev, "out")
+        rc = lib.r2l_act8_unpack(pq, ldq, _vec(scales, (M, -(-cols // ACT8_GROUP)), dev, "scales", torch.uint8),
+                                 _CODES[dtype], B, L, cols, _vec(lengths, (B,), dev, "lengths", torch.int32), po, ldo,
+                                 st)
+    if check and rc != 0:
+        raise R2LError(rc, "r2l_act8_unpack")
+    return out
