@@ -6,11 +6,18 @@
 
 #include "act8.cuh"
 #include "common.cuh"
+#include "gated_bwd.cuh"
+#include "gated_scan.cuh"
 #include "r2l.h"
 
 using r2l::bf16;
 using r2l::from_f32;
 using r2l::to_f32;
+using r2l::gated::BwdArgs;
+using r2l::gated::Ckpt;
+using r2l::gated::clamped_length;
+using r2l::gated::FwdArgs;
+using r2l::gated::MAX_CLUSTER;
 
 namespace {
 
@@ -28,144 +35,6 @@ bool aligned(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) == 0; }
       return R2L_ERR_CUDA;                  \
     }                                       \
   } while (0)
-
-// ------------------------------------------------------------------ device
-
-__device__ __forceinline__ int clamped_length(const int32_t* lengths, int b, int L) {
-  return lengths ? min(max(lengths[b], 0), L) : L;
-}
-
-// One block writes the status word: whether any length lies outside [0, L].
-__device__ __forceinline__ void write_status(const int32_t* lengths, int B, int L, uint32_t* status) {
-  int bad = 0;
-  if (lengths)
-    for (int b = threadIdx.x; b < B; b += blockDim.x) bad |= lengths[b] < 0 || lengths[b] > L;
-  bad = __syncthreads_or(bad);
-  if (threadIdx.x == 0) *status = bad ? R2L_DEVFLAG_LENGTH_CLAMPED : 0u;
-}
-
-__device__ __forceinline__ float sigmoid(float v) { return 1.0f / (1.0f + expf(-v)); }
-
-// −R2L_GATED_RATE · softplus(lam): the log of the decay at an open gate.
-__device__ __forceinline__ float decay_rate(float lam) {
-  return -R2L_GATED_RATE * (fmaxf(lam, 0.0f) + log1pf(expf(-fabsf(lam))));
-}
-
-struct Gates {
-  float a, beta, sr, sg, l;
-};
-__device__ __forceinline__ Gates gates(float r, float g, float rate) {
-  Gates q;
-  q.sr = sigmoid(r);
-  q.sg = sigmoid(g);
-  q.l = rate * q.sr;
-  q.a = expf(q.l);
-  q.beta = sqrtf(-expm1f(2.0f * q.l));
-  return q;
-}
-
-struct Ckpt {
-  float* states;        // [B][tiles][E]
-  uint8_t* q[3];        // x, r, g: [B·L][ldq]
-  uint8_t* scales[3];   // [B·L][ldq / GROUP]
-  int tiles, ldq;
-};
-
-struct FwdArgs {
-  const void *x, *r, *g;
-  long long ldx, ldr, ldg, ldy;
-  const float *lam, *h0;
-  void* y;
-  float* h_last;
-  int B, L, E, forward;
-  const int32_t* lengths;
-  uint32_t* status;
-  Ckpt ck;
-};
-
-struct BwdArgs {
-  const void *x, *r, *g, *dy;
-  long long ldx, ldr, ldg, ld_dy, ld_dx, ld_dr, ld_dg;
-  const float *lam, *dh_last;
-  void *dx, *dr, *dg;
-  float *dlam, *dh0, *part;
-  int B, L, E, forward, act8;
-  const int32_t* lengths;
-  uint32_t* status;
-  Ckpt ck;
-};
-
-template <typename T>
-__global__ void gated_fwd_kernel(FwdArgs p) {
-  if (p.status && blockIdx.x == 0 && blockIdx.y == 0) write_status(p.lengths, p.B, p.L, p.status);
-  const int e = blockIdx.x * blockDim.x + threadIdx.x, b = blockIdx.y;
-  if (e >= p.E) return;
-  const int n = clamped_length(p.lengths, b, p.L);
-  const float rate = decay_rate(p.lam[e]);
-  float h = p.h0 ? p.h0[(size_t)b * p.E + e] : 0.0f;
-  for (int k = 0; k < n; ++k) {
-    if (p.ck.states && k % TILE == 0) p.ck.states[((size_t)b * p.ck.tiles + k / TILE) * p.E + e] = h;
-    const long long m = (long long)b * p.L + (p.forward ? k : n - 1 - k);
-    const Gates q = gates(to_f32(((const T*)p.r)[m * p.ldr + e]), to_f32(((const T*)p.g)[m * p.ldg + e]), rate);
-    h = q.a * h + q.beta * q.sg * to_f32(((const T*)p.x)[m * p.ldx + e]);
-    ((T*)p.y)[m * p.ldy + e] = from_f32<T>(h);
-  }
-  if (p.h_last) p.h_last[(size_t)b * p.E + e] = h;
-}
-
-template <typename T>
-__device__ __forceinline__ float load_in(const BwdArgs& p, int which, const void* ptr, long long ld, long long m, int e) {
-  if (!p.act8) return to_f32(((const T*)ptr)[m * ld + e]);
-  const float up = r2l::act8::scale_up(p.ck.scales[which][m * (p.ck.ldq / GROUP) + e / GROUP]);
-  return r2l::act8::from_e4m3x2(p.ck.q[which][m * p.ck.ldq + e]).x * up;
-}
-
-template <typename T>
-__global__ void gated_bwd_kernel(BwdArgs p) {
-  if (blockIdx.x == 0 && blockIdx.y == 0) write_status(p.lengths, p.B, p.L, p.status);
-  const int e = blockIdx.x * blockDim.x + threadIdx.x, b = blockIdx.y;
-  if (e >= p.E) return;
-  const int n = clamped_length(p.lengths, b, p.L);
-  const float rate = decay_rate(p.lam[e]);
-  float D = p.dh_last ? p.dh_last[(size_t)b * p.E + e] : 0.0f, acc = 0.0f;
-  float enters[TILE];
-  for (int t = (n + TILE - 1) / TILE - 1; t >= 0; --t) {
-    float h = p.ck.states[((size_t)b * p.ck.tiles + t) * p.E + e];
-    const int k0 = t * TILE, k1 = min(n, k0 + TILE);
-    for (int k = k0; k < k1; ++k) {
-      const long long m = (long long)b * p.L + (p.forward ? k : n - 1 - k);
-      enters[k - k0] = h;
-      const Gates q = gates(load_in<T>(p, 1, p.r, p.ldr, m, e), load_in<T>(p, 2, p.g, p.ldg, m, e), rate);
-      h = q.a * h + q.beta * q.sg * load_in<T>(p, 0, p.x, p.ldx, m, e);
-    }
-    for (int k = k1 - 1; k >= k0; --k) {
-      const long long m = (long long)b * p.L + (p.forward ? k : n - 1 - k);
-      const float x = load_in<T>(p, 0, p.x, p.ldx, m, e);
-      const Gates q = gates(load_in<T>(p, 1, p.r, p.ldr, m, e), load_in<T>(p, 2, p.g, p.ldg, m, e), rate);
-      const float G = D + to_f32(((const T*)p.dy)[m * p.ld_dy + e]);
-      const float dl = q.l == 0.0f ? 0.0f : G * (q.a * enters[k - k0] - q.sg * x * q.a * q.a / q.beta);
-      ((T*)p.dx)[m * p.ld_dx + e] = from_f32<T>(G * q.beta * q.sg);
-      ((T*)p.dg)[m * p.ld_dg + e] = from_f32<T>(G * q.beta * x * q.sg * (1.0f - q.sg));
-      ((T*)p.dr)[m * p.ld_dr + e] = from_f32<T>(dl * q.l * (1.0f - q.sr));
-      acc += dl * q.sr;
-      D = G * q.a;
-    }
-  }
-  for (int i = n; i < p.L; ++i) {
-    const long long m = (long long)b * p.L + i;
-    ((T*)p.dx)[m * p.ld_dx + e] = ((T*)p.dg)[m * p.ld_dg + e] = ((T*)p.dr)[m * p.ld_dr + e] = from_f32<T>(0.0f);
-  }
-  p.part[(size_t)b * p.E + e] = acc;
-  if (p.dh0) p.dh0[(size_t)b * p.E + e] = D;
-}
-
-__global__ void gated_dlam_kernel(const float* part, int rows, const float* lam, int E, float* dlam) {
-  const int e = blockIdx.x * blockDim.x + threadIdx.x;
-  if (e >= E) return;
-  float s = 0.0f;
-  for (int i = 0; i < rows; ++i) s += part[(size_t)i * E + e];
-  dlam[e] = s * -R2L_GATED_RATE * sigmoid(lam[e]);
-}
 
 // A warp per (row, group), two channels a lane.
 template <typename T>
@@ -223,22 +92,22 @@ size_t elem_bytes(r2l_dtype t) { return t == R2L_BF16 ? 2 : 4; }
 // Byte offsets of a checkpoint's parts.
 struct CkptPlan {
   size_t states, q[3], scales[3], total;
-  int tiles, ldq;
+  int tiles, Lp;
 };
 CkptPlan plan_checkpoint(const r2l_dims* d, int B, int L) {
   CkptPlan k{};
-  const size_t M = (size_t)B * L, E = d->d_inner;
+  const size_t strips = align_up(d->d_inner, GROUP) / GROUP;
   k.tiles = (L - 1) / TILE + 1;
-  k.ldq = (int)align_up(E, GROUP);
+  k.Lp = (int)align_up(L, 16);
   size_t off = 0;
   k.states = off;
-  off = align_up(off + (size_t)B * k.tiles * E * sizeof(float), kAlign);
+  off = align_up(off + B * k.tiles * strips * GROUP * sizeof(float), kAlign);
   if (d->flags & R2L_FLAG_ACT8)
     for (int i = 0; i < 3; ++i) {
       k.q[i] = off;
-      off = align_up(off + M * k.ldq, kAlign);
+      off = align_up(off + B * strips * L * GROUP, kAlign);
       k.scales[i] = off;
-      off = align_up(off + M * (k.ldq / GROUP), kAlign);
+      off = align_up(off + B * strips * k.Lp, kAlign);
     }
   k.total = off;
   return k;
@@ -252,8 +121,72 @@ Ckpt checkpoint_at(const CkptPlan& k, void* base) {
     ck.scales[i] = (uint8_t*)(c + k.scales[i]);
   }
   ck.tiles = k.tiles;
-  ck.ldq = k.ldq;
+  ck.Lp = k.Lp;
   return ck;
+}
+
+// Blocks of a cluster that share a sequence's 64 channels.
+uint32_t cluster_blocks(int B, int strips, int L, int slots) {
+  const int tiles = (L - 1) / TILE + 1;
+  uint32_t c = 1;
+  while (c < MAX_CLUSTER && 2 * c <= (uint32_t)tiles && (long long)B * strips * c < slots) c *= 2;
+  return c;
+}
+
+template <typename Args>
+r2l_status launch(void (*kern)(Args, uint32_t), const Args& p, uint32_t blocks, int threads, size_t smem, cudaStream_t st) {
+  const long long grid = (long long)p.B * p.strips * blocks;
+  if (grid > 2147483647LL) return R2L_ERR_UNSUPPORTED;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return R2L_ERR_CUDA;
+  }
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = blocks;
+  attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kern, p, blocks) != cudaSuccess) {
+    (void)cudaGetLastError();
+    return R2L_ERR_CUDA;
+  }
+  return R2L_OK;
+}
+
+// Rows that start on 16-byte boundaries.
+bool rows16(const void* p, long long ld, size_t size) { return aligned(p, 16) && ld * size % 16 == 0; }
+
+template <typename T, bool VEC>
+r2l_status run_forward(const FwdArgs& p, int mode, cudaStream_t st) {
+  using namespace r2l::gated;
+  if (mode == 0 && p.L <= WALK_MAX) {
+    const long long grid = ((long long)p.B * ((p.E + 1) / 2) + 127) / 128;
+    if (grid > 2147483647LL) return R2L_ERR_UNSUPPORTED;
+    gated_walk_kernel<T, VEC><<<(unsigned)grid, 128, 0, st>>>(p);
+    R2L_LAUNCH_CHECK();
+    return R2L_OK;
+  }
+  const uint32_t c = cluster_blocks(p.B, p.strips, p.L, 148 * (sizeof(T) == 2 ? 4 : 2));
+  const size_t smem = sizeof(FwdSmem<T>) + box_bytes(c);
+  if (mode == 0) return launch(gated_scan_kernel<T, VEC, 0>, p, c, FW * 32, smem, st);
+  if (mode == 1) return launch(gated_scan_kernel<T, VEC, 1>, p, c, FW * 32, smem, st);
+  return launch(gated_scan_kernel<T, VEC, 2>, p, c, FW * 32, smem, st);
+}
+
+uint32_t backward_blocks(const r2l_dims* d, int B, int L) {
+  return cluster_blocks(B, (d->d_inner - 1) / GROUP + 1, L, 148 * (d->dtype == R2L_BF16 ? 2 : 1));
+}
+
+template <typename T, bool VEC, bool ACT8>
+r2l_status run_backward(const BwdArgs& p, uint32_t c, cudaStream_t st) {
+  using namespace r2l::gated;
+  return launch(gated_bwd_kernel<T, VEC, ACT8>, p, c, BW * 32, sizeof(BwdSmem<T, ACT8>) + box_bytes(c), st);
 }
 
 // Rows of E elements of `size` bytes with stride ld.
@@ -295,34 +228,31 @@ r2l_status forward_impl(const r2l_gated_in* in, void* y, int ldy, float* h_last,
   if (!aligned(in->lam, 4) || !aligned(in->h0, 4) || !aligned(h_last, 4) || !aligned(lengths, 4) ||
       !aligned(status, 4))
     return R2L_ERR_ALIGNMENT;
-  if (!fits(B, L, E) || B > 65535) return R2L_ERR_UNSUPPORTED;
+  if (!fits(B, L, E)) return R2L_ERR_UNSUPPORTED;
   FwdArgs p{};
   p.x = in->x; p.r = in->r; p.g = in->g;
   p.ldx = in->ldx; p.ldr = in->ldr; p.ldg = in->ldg; p.ldy = ldy;
   p.lam = in->lam; p.h0 = in->h0; p.y = y; p.h_last = h_last;
-  p.B = B; p.L = L; p.E = E; p.forward = (dims->flags & R2L_FLAG_FORWARD_SCAN) ? 1 : 0;
+  p.B = B; p.L = L; p.E = E; p.strips = (E - 1) / GROUP + 1;
+  p.forward = (dims->flags & R2L_FLAG_FORWARD_SCAN) ? 1 : 0;
   p.lengths = lengths; p.status = status;
-  cudaStream_t st = (cudaStream_t)stream;
   if (train) {
     const CkptPlan k = plan_checkpoint(dims, B, L);
     if (!checkpoint || checkpoint_bytes < k.total) return R2L_ERR_WORKSPACE;
     if (!aligned(checkpoint, 16)) return R2L_ERR_ALIGNMENT;
     p.ck = checkpoint_at(k, checkpoint);
   }
-  if (train && (dims->flags & R2L_FLAG_ACT8)) {
-    const void* src[3] = {in->x, in->r, in->g};
-    const int ld[3] = {in->ldx, in->ldr, in->ldg};
-    for (int i = 0; i < 3; ++i)
-      R2L_TRY(act8_pack(src[i], ld[i], dims->dtype, B, L, E, lengths, p.ck.q[i], p.ck.ldq, p.ck.scales[i], st));
-  }
-  const dim3 grid((E + 63) / 64, B);
-  if (dims->dtype == R2L_BF16) gated_fwd_kernel<bf16><<<grid, 64, 0, st>>>(p);
-  else gated_fwd_kernel<float><<<grid, 64, 0, st>>>(p);
-  R2L_LAUNCH_CHECK();
-  return R2L_OK;
+  const int mode = !train ? 0 : (dims->flags & R2L_FLAG_ACT8) ? 2 : 1;
+  const bool vec = rows16(p.x, p.ldx, es) && rows16(p.r, p.ldr, es) && rows16(p.g, p.ldg, es) && rows16(p.y, p.ldy, es);
+  cudaStream_t st = (cudaStream_t)stream;
+  if (dims->dtype == R2L_BF16) return vec ? run_forward<bf16, true>(p, mode, st) : run_forward<bf16, false>(p, mode, st);
+  return vec ? run_forward<float, true>(p, mode, st) : run_forward<float, false>(p, mode, st);
 }
 
-size_t part_bytes(const r2l_dims* d, int B) { return (size_t)B * d->d_inner * sizeof(float); }
+// Shares of dlam, one row for each block of channels' blocks.
+size_t part_bytes(const r2l_dims* d, int B, int L) {
+  return (size_t)B * backward_blocks(d, B, L) * align_up(d->d_inner, GROUP) * sizeof(float);
+}
 
 }  // namespace
 
@@ -344,7 +274,7 @@ r2l_status r2l_gated_scan_train(const r2l_gated_in* in, void* y, int ldy, float*
 }
 
 size_t r2l_gated_scan_backward_workspace_size(const r2l_dims* dims, int B, int L) {
-  return valid_dims(dims, B, L) && fits(B, L, dims->d_inner) ? kAlign + align_up(part_bytes(dims, B), kAlign) : 0;
+  return valid_dims(dims, B, L) && fits(B, L, dims->d_inner) ? kAlign + align_up(part_bytes(dims, B, L), kAlign) : 0;
 }
 
 r2l_status r2l_gated_scan_backward(const r2l_gated_in* in, const void* dy, int ld_dy, const float* dh_last,
@@ -376,7 +306,7 @@ r2l_status r2l_gated_scan_backward(const r2l_gated_in* in, const void* dy, int l
   if (!aligned(in->lam, 4) || !aligned(dh_last, 4) || !aligned(grads->dlam, 4) || !aligned(grads->dh0, 4) ||
       !aligned(lengths, 4))
     return R2L_ERR_ALIGNMENT;
-  if (!fits(B, L, E) || B > 65535) return R2L_ERR_UNSUPPORTED;
+  if (!fits(B, L, E)) return R2L_ERR_UNSUPPORTED;
   const CkptPlan k = plan_checkpoint(dims, B, L);
   if (!checkpoint || checkpoint_bytes < k.total) return R2L_ERR_WORKSPACE;
   if (!workspace || workspace_bytes < r2l_gated_scan_backward_workspace_size(dims, B, L)) return R2L_ERR_WORKSPACE;
@@ -386,17 +316,25 @@ r2l_status r2l_gated_scan_backward(const r2l_gated_in* in, const void* dy, int l
   p.ldx = in->ldx; p.ldr = in->ldr; p.ldg = in->ldg; p.ld_dy = ld_dy;
   p.dx = grads->dx; p.dr = grads->dr; p.dg = grads->dg;
   p.ld_dx = grads->ld_dx; p.ld_dr = grads->ld_dr; p.ld_dg = grads->ld_dg;
-  p.lam = in->lam; p.dh_last = dh_last; p.dlam = grads->dlam; p.dh0 = grads->dh0;
+  p.lam = in->lam; p.dh_last = dh_last; p.dh0 = grads->dh0;
   p.part = (float*)((char*)workspace + kAlign);
-  p.B = B; p.L = L; p.E = E; p.forward = (dims->flags & R2L_FLAG_FORWARD_SCAN) ? 1 : 0; p.act8 = act8;
+  p.B = B; p.L = L; p.E = E; p.strips = (E - 1) / GROUP + 1;
+  p.forward = (dims->flags & R2L_FLAG_FORWARD_SCAN) ? 1 : 0;
   p.lengths = lengths; p.status = (uint32_t*)workspace;
   p.ck = checkpoint_at(k, const_cast<void*>(checkpoint));
+  const bool vec = (act8 || (rows16(p.x, p.ldx, es) && rows16(p.r, p.ldr, es) && rows16(p.g, p.ldg, es))) &&
+                   rows16(p.dy, p.ld_dy, es) && rows16(p.dx, p.ld_dx, es) && rows16(p.dr, p.ld_dr, es) &&
+                   rows16(p.dg, p.ld_dg, es);
+  const uint32_t c = backward_blocks(dims, B, L);
   cudaStream_t st = (cudaStream_t)stream;
-  const dim3 grid((E + 63) / 64, B);
-  if (dims->dtype == R2L_BF16) gated_bwd_kernel<bf16><<<grid, 64, 0, st>>>(p);
-  else gated_bwd_kernel<float><<<grid, 64, 0, st>>>(p);
-  R2L_LAUNCH_CHECK();
-  gated_dlam_kernel<<<(E + 127) / 128, 128, 0, st>>>(p.part, B, p.lam, E, p.dlam);
+  if (dims->dtype == R2L_BF16) {
+    if (act8) R2L_TRY((vec ? run_backward<bf16, true, true> : run_backward<bf16, false, true>)(p, c, st));
+    else R2L_TRY((vec ? run_backward<bf16, true, false> : run_backward<bf16, false, false>)(p, c, st));
+  } else {
+    if (act8) R2L_TRY((vec ? run_backward<float, true, true> : run_backward<float, false, true>)(p, c, st));
+    else R2L_TRY((vec ? run_backward<float, true, false> : run_backward<float, false, false>)(p, c, st));
+  }
+  r2l::gated::gated_dlam_kernel<<<(E + 31) / 32, 256, 0, st>>>(p.part, (int)(B * c), p.strips * GROUP, p.lam, E, grads->dlam);
   R2L_LAUNCH_CHECK();
   return R2L_OK;
 }

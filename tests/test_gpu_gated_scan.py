@@ -313,7 +313,7 @@ def test_extreme_gates(dtype, L):
     check_forward(d, y, h, B, L, False)
     assert torch.equal(h[:, 0].cpu(), d["h0"][:, 0]) and torch.equal(h[:, 4].cpu(), d["h0"][:, 4])
     for k, v in out.items():
-        assert torch.isfinite(v.float()).all(), k
+        assert bool(torch.isfinite(v.float()).all()), k
     check_backward(d, out, B, L, False)
     dims = bd.gated_dims(E, dtype)
     c = dev(d)
