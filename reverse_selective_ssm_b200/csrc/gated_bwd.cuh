@@ -18,6 +18,33 @@ constexpr int BW = 8;              // warps of a gradient block
 constexpr int BP = TILE / BW;      // rows of a warp
 constexpr float TINY = 1.17549435e-38f;
 
+// A tile of rows into dst[TILE][STRIP]: row k from src + k · step, its first
+// `cols` channels; rows from `rows` on are filled with `fill` (bf16 holds it).
+// VEC: every row starts on a 16-byte boundary.
+template <typename T, bool VEC, int THREADS>
+__device__ __forceinline__ void load_tile(T* dst, const T* src, long long step, int rows, int cols, float fill) {
+  if (VEC) {
+    constexpr int PER = 16 / (int)sizeof(T), CHUNKS = STRIP / PER;
+#pragma unroll
+    for (int i = 0; i < TILE * CHUNKS / THREADS; ++i) {
+      const int row = (threadIdx.x + i * THREADS) / CHUNKS, c = (threadIdx.x + i * THREADS) % CHUNKS * PER;
+      T* at = dst + row * STRIP + c;
+      if (row < rows) {
+        const int bytes = min(max(cols - c, 0), PER) * (int)sizeof(T);
+        copy16(at, bytes ? src + row * step + c : src, bytes);
+      } else {
+        const uint32_t f = bits_twice<T>(fill);
+        *reinterpret_cast<uint4*>(at) = make_uint4(f, f, f, f);
+      }
+    }
+  } else {
+    for (int i = threadIdx.x; i < TILE * STRIP; i += THREADS) {
+      const int row = i / STRIP, c = i % STRIP;
+      dst[i] = row < rows && c < cols ? src[row * step + c] : from_f32<T>(row < rows ? 0.0f : fill);
+    }
+  }
+}
+
 template <typename T, bool ACT8>
 struct BwdSmem {
   typedef typename std::conditional<ACT8, uint8_t, T>::type Q;
@@ -33,6 +60,8 @@ __device__ __forceinline__ float2 lane_pair8(const uint8_t* row, int lane, uint3
   return __fmul2_rn(act8::from_e4m3x2(reinterpret_cast<const uint16_t*>(row)[lane]), two(act8::scale_up(scale)));
 }
 
+constexpr size_t box_bytes(uint32_t blocks) { return blocks > 1 ? 2 * (size_t)blocks * 32 * sizeof(float4) : 0; }
+
 template <typename T, bool VEC, bool ACT8>
 __global__ void __launch_bounds__(BW * 32, 2) gated_bwd_kernel(const BwdArgs p, const uint32_t blocks) {
   extern __shared__ __align__(16) unsigned char smem_raw[];
@@ -42,14 +71,12 @@ __global__ void __launch_bounds__(BW * 32, 2) gated_bwd_kernel(const BwdArgs p, 
   const uint32_t rank = blockIdx.x % blocks;
   const uint32_t job = blockIdx.x / blocks;
   const int strip = (int)(job % (uint32_t)p.strips), b = (int)(job / (uint32_t)p.strips);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
   const int e0 = strip * STRIP, cols = min(p.E - e0, STRIP);
   const int n = clamped_length(p.lengths, b, p.L);
   const long long row0 = (long long)b * p.L + (p.forward ? 0 : n - 1);
   const int dir = p.forward ? 1 : -1;
-  const float2 lam = load_vec_pair(p.lam + e0, lane, cols);
-  const float2 rate = make_float2(decay_rate(lam.x), decay_rate(lam.y));
-  const float2 rate2 = __fmul2_rn(rate, two(LOG2E));
+  const float2 rate = decay_rates(p.lam + e0, lane, cols), rate2 = __fmul2_rn(rate, two(LOG2E));
   float2 carry = p.dh_last ? load_vec_pair(p.dh_last + (size_t)b * p.E + e0, lane, cols) : two(0.0f);
   float2 dlam = two(0.0f);
 
@@ -127,7 +154,7 @@ __global__ void __launch_bounds__(BW * 32, 2) gated_bwd_kernel(const BwdArgs p, 
       float4 whole = sm.maps[BW - 1][lane];
 #pragma unroll
       for (int w = BW - 2; w >= 0; --w) whole = after(sm.maps[w][lane], whole);
-      D = through_cluster(box + buf * blocks * 32, whole, warp, BW, lane, rank, blocks, carry);
+      D = through_cluster(box + buf * blocks * 32, whole, warp, BW, lane, 32, rank, blocks, carry);
     } else {
       D = carry;
 #pragma unroll

@@ -134,8 +134,9 @@ uint32_t cluster_blocks(int B, int strips, int L, int slots) {
 }
 
 template <typename Args>
-r2l_status launch(void (*kern)(Args, uint32_t), const Args& p, uint32_t blocks, int threads, size_t smem, cudaStream_t st) {
-  const long long grid = (long long)p.B * p.strips * blocks;
+r2l_status launch(void (*kern)(Args, uint32_t), const Args& p, long long jobs, uint32_t blocks, int threads, size_t smem,
+                  cudaStream_t st) {
+  const long long grid = jobs * blocks;
   if (grid > 2147483647LL) return R2L_ERR_UNSUPPORTED;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
     (void)cudaGetLastError();
@@ -172,11 +173,14 @@ r2l_status run_forward(const FwdArgs& p, int mode, cudaStream_t st) {
     R2L_LAUNCH_CHECK();
     return R2L_OK;
   }
-  const uint32_t c = cluster_blocks(p.B, p.strips, p.L, 148 * (sizeof(T) == 2 ? 4 : 2));
-  const size_t smem = sizeof(FwdSmem<T>) + box_bytes(c);
-  if (mode == 0) return launch(gated_scan_kernel<T, VEC, 0>, p, c, FW * 32, smem, st);
-  if (mode == 1) return launch(gated_scan_kernel<T, VEC, 1>, p, c, FW * 32, smem, st);
-  return launch(gated_scan_kernel<T, VEC, 2>, p, c, FW * 32, smem, st);
+  const int strips32 = (p.E - 1) / 32 + 1;
+  if (mode == 2) {
+    const uint32_t c = cluster_blocks(p.B, p.strips, p.L, 148 * (sizeof(T) == 2 ? 3 : 2));
+    return launch(gated_scan_kernel<T, VEC, 2, 32>, p, (long long)p.B * p.strips, c, FG * 32, fwd_smem_bytes<T, 32>(c), st);
+  }
+  const uint32_t c = cluster_blocks(p.B, strips32, p.L, 148 * (sizeof(T) == 2 ? 7 : 4));
+  return launch(mode == 0 ? gated_scan_kernel<T, VEC, 0, 16> : gated_scan_kernel<T, VEC, 1, 16>, p, (long long)p.B * strips32,
+                c, FG * 16, fwd_smem_bytes<T, 16>(c), st);
 }
 
 uint32_t backward_blocks(const r2l_dims* d, int B, int L) {
@@ -186,7 +190,7 @@ uint32_t backward_blocks(const r2l_dims* d, int B, int L) {
 template <typename T, bool VEC, bool ACT8>
 r2l_status run_backward(const BwdArgs& p, uint32_t c, cudaStream_t st) {
   using namespace r2l::gated;
-  return launch(gated_bwd_kernel<T, VEC, ACT8>, p, c, BW * 32, sizeof(BwdSmem<T, ACT8>) + box_bytes(c), st);
+  return launch(gated_bwd_kernel<T, VEC, ACT8>, p, (long long)p.B * p.strips, c, BW * 32, sizeof(BwdSmem<T, ACT8>) + box_bytes(c), st);
 }
 
 // Rows of E elements of `size` bytes with stride ld.

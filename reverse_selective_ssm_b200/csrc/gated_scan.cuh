@@ -20,6 +20,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "act8.cuh"
 #include "common.cuh"
 #include "r2l.h"
@@ -28,7 +30,7 @@ namespace r2l {
 namespace gated {
 
 constexpr int TILE = R2L_GATED_TILE;     // positions per tile, and between two states of a checkpoint
-constexpr int STRIP = R2L_ACT8_GROUP;    // channels per block: two per lane, and one scale of an 8-bit checkpoint
+constexpr int STRIP = R2L_ACT8_GROUP;    // channels that share a scale of an 8-bit checkpoint
 constexpr int MAX_CLUSTER = 8;           // the portable limit
 constexpr int WALK_MAX = 8;              // positions up to which a thread walks a sequence by itself
 static_assert(STRIP == 64, "a lane holds two channels");
@@ -93,22 +95,24 @@ __device__ __forceinline__ float rsqrt_approx(float x) {
 }
 __device__ __forceinline__ float2 two(float v) { return make_float2(v, v); }
 
-// −R2L_GATED_RATE · softplus(lam): log a at an open gate.
 __device__ __forceinline__ float decay_rate(float lam) {
   return -R2L_GATED_RATE * (fmaxf(lam, 0.0f) + log1pf(expf(-fabsf(lam))));
 }
 
-// 1 / (1 + 2^(−v log2 e)): 0 at −∞ and 1 at +∞.
-__device__ __forceinline__ float2 sigmoid2(float2 v) {
+// 1 + 2^(−v log2 e), whose reciprocal is σ(v): ∞ at −∞ and 1 at +∞.
+__device__ __forceinline__ float2 sigmoid_den(float2 v) {
   const float2 t = __fmul2_rn(v, two(-LOG2E));
-  const float2 d = __fadd2_rn(make_float2(ex2(t.x), ex2(t.y)), two(1.0f));
+  return __fadd2_rn(make_float2(ex2(t.x), ex2(t.y)), two(1.0f));
+}
+__device__ __forceinline__ float2 sigmoid2(float2 v) {
+  const float2 d = sigmoid_den(v);
   return make_float2(rcp(d.x), rcp(d.y));
 }
 
-// The two channels of a lane at one position.  u = 1 − a² = −expm1(2 log a):
-// above 2 log a = −1/4 the subtraction would lose the digits that matter (a
-// channel with a memory of 1000 positions has 1 − a² = 0.002), so the Taylor
-// polynomial of degree 6 is taken there (relative error under 5e-8).
+// Any decay: u = 1 − a² = −expm1(2 log a).  Where a is near 1 the subtraction
+// would lose the digits that matter (a channel with a memory of 1000 positions
+// has 1 − a² = 0.002), so for log2 a above −0.18 it is a polynomial in log2 a
+// without a constant term, fitted for the least relative error (4 · 2^-24).
 struct Gates {
   float2 a, u, sr, sg;
 };
@@ -118,16 +122,54 @@ __device__ __forceinline__ Gates gates2(float2 r, float2 g, float2 rate2 /* rate
   q.sg = sigmoid2(g);
   const float2 l2 = __fmul2_rn(q.sr, rate2);
   q.a = make_float2(ex2(l2.x), ex2(l2.y));
-  const float2 t = __fmul2_rn(l2, two(2.0f * LN2));
-  const float2 far = __ffma2_rn(make_float2(-q.a.x, -q.a.y), q.a, two(1.0f));
-  float2 c = __ffma2_rn(t, two(-1.0f / 720.0f), two(-1.0f / 120.0f));
-  c = __ffma2_rn(c, t, two(-1.0f / 24.0f));
-  c = __ffma2_rn(c, t, two(-1.0f / 6.0f));
-  c = __ffma2_rn(c, t, two(-0.5f));
-  c = __ffma2_rn(c, t, two(-1.0f));
-  c = __fmul2_rn(c, t);
-  q.u = make_float2(t.x > -0.25f ? c.x : far.x, t.y > -0.25f ? c.y : far.y);
+  const float2 far = __ffma2_rn(__fmul2_rn(q.a, q.a), two(-1.0f), two(1.0f));
+  float2 c = __ffma2_rn(l2, two(-0.139302522f), two(-0.442409396f));
+  c = __ffma2_rn(c, l2, two(-0.960847378f));
+  c = __ffma2_rn(c, l2, two(-1.38629401f));
+  c = __fmul2_rn(c, l2);
+  q.u = make_float2(l2.x > -0.18f ? c.x : far.x, l2.y > -0.18f ? c.y : far.y);
   return q;
+}
+
+// Channels that keep at least 0.71 of their state per position at an open gate
+// (−0.5 ≤ rate2 ≤ 0; a recurrence with a memory of a few positions or more).
+// With s = 1/√(1 + e^−r), σ(r) = s² and β = s · k · p(log2 a), where
+// k = √(−2 ln 2 · rate2) and p is smooth: one reciprocal square root gives the
+// gate and β's square root, and a is a polynomial too, so a position takes four
+// special-function operations instead of six, and no choice by cases.  Both
+// polynomials are fitted on [−0.5, 0] for the least relative error (under 2^-24).
+constexpr float NEAR_RATE2 = -0.5f;
+__device__ __forceinline__ float2 near_decay(float2 l2) {   // 2^l2
+  float2 c = __ffma2_rn(l2, two(0.00115445221f), two(0.0095412815f));
+  c = __ffma2_rn(c, l2, two(0.0554904081f));
+  c = __ffma2_rn(c, l2, two(0.240225643f));
+  c = __ffma2_rn(c, l2, two(0.693147182f));
+  return __ffma2_rn(c, l2, two(1.0f));
+}
+__device__ __forceinline__ float2 near_beta(float2 l2) {    // √((1 − 2^(2 l2)) / (−2 ln 2 · l2))
+  float2 c = __ffma2_rn(l2, two(0.00273338961f), two(0.0206286889f));
+  c = __ffma2_rn(c, l2, two(0.100061379f));
+  c = __ffma2_rn(c, l2, two(0.346571505f));
+  return __ffma2_rn(c, l2, two(1.0f));
+}
+__device__ __forceinline__ float2 near_scale(float2 rate2) {   // k
+  return make_float2(sqrtf(-2.0f * LN2 * rate2.x), sqrtf(-2.0f * LN2 * rate2.y));
+}
+
+// a and b = β σ(g) x at one position.
+template <bool NEAR>
+__device__ __forceinline__ void coefficients(float2 x, float2 r, float2 g, float2 rate2, float2 k, float2& a, float2& b) {
+  if (NEAR) {
+    const float2 d = sigmoid_den(r);
+    const float2 s = make_float2(rsqrt_approx(d.x), rsqrt_approx(d.y));
+    const float2 l2 = __fmul2_rn(__fmul2_rn(s, s), rate2);
+    a = near_decay(l2);
+    b = __fmul2_rn(__fmul2_rn(__fmul2_rn(s, k), near_beta(l2)), __fmul2_rn(sigmoid2(g), x));
+  } else {
+    const Gates q = gates2(r, g, rate2);
+    a = q.a;
+    b = __fmul2_rn(make_float2(sqrt_approx(q.u.x), sqrt_approx(q.u.y)), __fmul2_rn(q.sg, x));
+  }
 }
 
 // ---------------------------------------------------------------- data movement
@@ -168,29 +210,71 @@ __device__ __forceinline__ uint32_t bits_twice<bf16>(float v) {
   return (__float_as_uint(v) >> 16) * 0x10001u;
 }
 
-// A tile of rows into dst[TILE][STRIP]: row k from src + k · step, its first
-// `cols` channels; rows from `rows` on are filled with `fill` (bf16 holds it).
-// VEC: every row starts on a 16-byte boundary.
-template <typename T, bool VEC, int THREADS>
-__device__ __forceinline__ void load_tile(T* dst, const T* src, long long step, int rows, int cols, float fill) {
-  if (VEC) {
-    constexpr int PER = 16 / (int)sizeof(T), CHUNKS = STRIP / PER;
+// Threads of a warp and their rows.  LANES lanes hold a row of 2 · LANES
+// channels, two each, so a warp has 32 / LANES groups of ROWS consecutive rows;
+// in shared memory a group is followed by 64 bytes of nothing, which puts two
+// groups that are read together into different banks.
+template <typename T, int LANES, int ROWS>
+struct Layout {
+  static constexpr int CHANNELS = 2 * LANES;
+  static constexpr int GROUP_STRIDE = ROWS * CHANNELS + (LANES < 32 ? 64 / (int)sizeof(T) : 0);   // elements
+  static constexpr int PER = 16 / (int)sizeof(T);            // elements of a copy
+  static constexpr int CHUNKS = CHANNELS / PER;              // copies of a row
+  static constexpr int AT_ONCE = 32 / CHUNKS;                // rows that a warp's lanes copy at once
+  static constexpr int WARP_ROWS = ROWS * (32 / LANES);
+  static_assert(ROWS % AT_ONCE == 0, "a copy of the warp's lanes stays within a group");
+  static __device__ __forceinline__ int at(int row) { return row / ROWS * GROUP_STRIDE + row % ROWS * CHANNELS; }
+};
+
+// The rows of one warp on their way to shared memory.  A warp copies only the
+// rows that it reads itself, so a copy needs no barrier of the block, and its
+// address is a pointer that moves from tile to tile.
+template <typename T, bool VEC, typename LAY>
+struct RowStream {
+  const T* at;            // VEC: this lane's chunk of the next tile's first rows; else the warp's first row
+  long long step, leap;   // to the next row, and to the next tile
+  __device__ __forceinline__ void start(const void* base, long long row, long long ld, int dir, int e0, long long tile_rows,
+                                        int lane) {
+    step = dir * ld;
+    leap = tile_rows * step;
+    at = (const T*)base + row * ld + e0 + (VEC ? lane / LAY::CHUNKS * step + lane % LAY::CHUNKS * LAY::PER : 0);
+  }
+  // The next tile's rows into dst.
+  __device__ __forceinline__ void whole(T* dst, int lane) const {
+    dst += lane * LAY::PER;    // chunk `lane` of AT_ONCE whole rows
 #pragma unroll
-    for (int i = 0; i < TILE * CHUNKS / THREADS; ++i) {
-      const int row = (threadIdx.x + i * THREADS) / CHUNKS, c = (threadIdx.x + i * THREADS) % CHUNKS * PER;
-      T* at = dst + row * STRIP + c;
-      if (row < rows) {
-        const int bytes = min(max(cols - c, 0), PER) * (int)sizeof(T);
-        copy16(at, bytes ? src + row * step + c : src, bytes);
+    for (int i = 0; i < LAY::WARP_ROWS; i += LAY::AT_ONCE) copy16(dst + LAY::at(i), at + i * step, 16);
+  }
+};
+
+__device__ __forceinline__ void copy_element(float* to, const float* from) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(to)), "l"(from) : "memory");
+}
+__device__ __forceinline__ void copy_element(bf16* to, const bf16* from) { *to = *from; }
+
+// The same where the tile has `rows` valid rows or `cols` channels only, or
+// where rows are not aligned: what lies past them is 0, and `fill` in rows past
+// the end (bf16 holds it).
+template <typename T, bool VEC, typename LAY>
+__device__ __noinline__ void copy_part(T* dst, const T* at, long long step, int lane, int rows, int cols, float fill) {
+  if (VEC) {
+    const int c = lane % LAY::CHUNKS * LAY::PER, bytes = min(max(cols - c, 0), LAY::PER) * (int)sizeof(T);
+    for (int i = 0; i < LAY::WARP_ROWS; i += LAY::AT_ONCE) {
+      T* const to = dst + lane * LAY::PER + LAY::at(i);
+      if (lane / LAY::CHUNKS + i < rows) {
+        copy16(to, bytes ? at + i * step : at - c, bytes);
       } else {
         const uint32_t f = bits_twice<T>(fill);
-        *reinterpret_cast<uint4*>(at) = make_uint4(f, f, f, f);
+        *reinterpret_cast<uint4*>(to) = make_uint4(f, f, f, f);
       }
     }
   } else {
-    for (int i = threadIdx.x; i < TILE * STRIP; i += THREADS) {
-      const int row = i / STRIP, c = i % STRIP;
-      dst[i] = row < rows && c < cols ? src[row * step + c] : from_f32<T>(row < rows ? 0.0f : fill);
+#pragma unroll 16
+    for (int i = 0; i < LAY::WARP_ROWS * LAY::CHANNELS; i += 32) {
+      const int row = (i + lane) / LAY::CHANNELS, c = (i + lane) % LAY::CHANNELS;
+      T* const to = dst + LAY::at(row) + c;
+      if (row < rows && c < cols) copy_element(to, at + row * step + c);
+      else *to = from_f32<T>(row < rows ? 0.0f : fill);
     }
   }
 }
@@ -201,6 +285,11 @@ __device__ __forceinline__ float2 lane_pair(const float* row, int lane) {
 __device__ __forceinline__ float2 lane_pair(const bf16* row, int lane) {
   const uint32_t v = reinterpret_cast<const uint32_t*>(row)[lane];
   return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+}
+
+__device__ __forceinline__ void store_whole_pair(float* at, float2 v) { *reinterpret_cast<float2*>(at) = v; }
+__device__ __forceinline__ void store_whole_pair(bf16* at, float2 v) {
+  *reinterpret_cast<__nv_bfloat162*>(at) = __float22bfloat162_rn(v);
 }
 
 // Channels 2·lane and 2·lane + 1 of a row of `cols` channels.  VEC: the pair is aligned.
@@ -232,6 +321,12 @@ __device__ __forceinline__ float2 load_vec_pair(const float* v, int lane, int co
   return make_float2(2 * lane < cols ? v[2 * lane] : 0.0f, 2 * lane + 1 < cols ? v[2 * lane + 1] : 0.0f);
 }
 
+// −R2L_GATED_RATE · softplus(lam), log a at an open gate; 0 for channels past the last.
+__device__ __forceinline__ float2 decay_rates(const float* lam, int lane, int cols) {
+  return make_float2(2 * lane < cols ? decay_rate(lam[2 * lane]) : 0.0f,
+                     2 * lane + 1 < cols ? decay_rate(lam[2 * lane + 1]) : 0.0f);
+}
+
 // ---------------------------------------------------------------- clusters
 
 __device__ __forceinline__ void cluster_sync() {
@@ -259,144 +354,180 @@ __device__ __forceinline__ float4 after(float4 second, float4 first) {
 // The tiles' maps of one round through the cluster: `mine` is this block's, and
 // `carry` the value that enters the first block's tile; returns the value that
 // enters this block's and moves carry past the last block's.  box holds
-// [blocks][32] maps and alternates between two buffers from round to
+// [blocks][lanes] maps and alternates between two buffers from round to
 // round: a block writes a buffer again only after the barrier of the round
 // between, which every reader of the buffer has passed.
-__device__ __forceinline__ float2 through_cluster(float4* box, float4 mine, int warp, int warps, int lane, uint32_t rank,
-                                                  uint32_t blocks, float2& carry) {
-  for (uint32_t to = warp; to < blocks; to += warps) store_to_rank(box + rank * 32 + lane, to, mine);
+__device__ __forceinline__ float2 through_cluster(float4* box, float4 mine, int group, int groups, int lane, int lanes,
+                                                  uint32_t rank, uint32_t blocks, float2& carry) {
+  for (uint32_t to = group; to < blocks; to += groups) store_to_rank(box + rank * lanes + lane, to, mine);
   cluster_sync();
   float2 enters = carry;
   for (uint32_t q = 0; q < blocks; ++q) {
     if (q == rank) enters = carry;
-    carry = apply(box[q * 32 + lane], carry);
+    carry = apply(box[q * lanes + lane], carry);
   }
   return enters;
 }
 
 // ---------------------------------------------------------------- forward
 
-constexpr int FW = 4;              // warps of a forward block
-constexpr int FP = TILE / FW;      // rows of a warp
+constexpr int FG = 8;              // groups of rows of a forward block
+constexpr int FP = TILE / FG;      // rows of a group
 
-template <typename T>
+// In shared memory, behind it the maps of the block's groups, [2][maps][LANES],
+// and of the cluster's blocks, [2][blocks][LANES].  A block by itself has no use
+// for its last group's map.
+template <typename T, int LANES>
 struct FwdSmem {
-  T in[2][3][TILE * STRIP];
-  float4 maps[FW][32];
+  T in[2][3][FG * Layout<T, LANES, FP>::GROUP_STRIDE];
+  float2 carry[2][LANES];
 };
-// The cluster's maps lie behind it: [2][blocks][32].
-constexpr size_t box_bytes(uint32_t blocks) { return blocks > 1 ? 2 * (size_t)blocks * 32 * sizeof(float4) : 0; }
+__host__ __device__ constexpr int group_maps(uint32_t blocks) { return blocks > 1 ? FG : FG - 1; }
+template <typename T, int LANES>
+constexpr size_t fwd_smem_bytes(uint32_t blocks) {
+  return sizeof(FwdSmem<T, LANES>) + 2 * sizeof(float4) * LANES * (group_maps(blocks) + (blocks > 1 ? blocks : 0));
+}
 
 // MODE 0: the recurrence; 1: also the states of a checkpoint; 2: and its 8 bits.
-template <typename T, bool VEC, int MODE>
-__global__ void __launch_bounds__(FW * 32, sizeof(T) == 2 ? 4 : 2) gated_scan_kernel(const FwdArgs p, const uint32_t blocks) {
+template <typename T, bool VEC, int MODE, int LANES>
+__global__ void __launch_bounds__(FG * LANES, (sizeof(T) == 2 ? 7 : 4) * 32 / LANES / 2)
+    gated_scan_kernel(const FwdArgs p, const uint32_t blocks) {
+  typedef Layout<T, LANES, FP> Lay;
+  static_assert(MODE < 2 || LANES == 32, "the channels of a scale are a row of the warp");
   extern __shared__ __align__(16) unsigned char smem_raw[];
-  FwdSmem<T>& sm = *reinterpret_cast<FwdSmem<T>*>(smem_raw);
-  float4* const box = reinterpret_cast<float4*>(smem_raw + sizeof(FwdSmem<T>));
+  FwdSmem<T, LANES>& sm = *reinterpret_cast<FwdSmem<T, LANES>*>(smem_raw);
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), wl = threadIdx.x & 31;   // uniform for the compiler too
+  const int lane = wl % LANES, group = warp * (32 / LANES) + wl / LANES;
+  const int nmaps = group_maps(blocks);
+  float4* const maps = reinterpret_cast<float4*>(smem_raw + sizeof(FwdSmem<T, LANES>)) + lane;
+  float4* const box = reinterpret_cast<float4*>(smem_raw + sizeof(FwdSmem<T, LANES>)) + 2 * nmaps * LANES;
   if (p.status && blockIdx.x == 0) write_status(p.lengths, p.B, p.L, p.status);
   const uint32_t rank = blockIdx.x % blocks;
   const uint32_t job = blockIdx.x / blocks;
-  const int strip = (int)(job % (uint32_t)p.strips), b = (int)(job / (uint32_t)p.strips);
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int e0 = strip * STRIP, cols = min(p.E - e0, STRIP);
+  const uint32_t strips = (uint32_t)(p.E - 1) / Lay::CHANNELS + 1;
+  const int b = (int)(job / strips), e0 = (int)(job % strips) * Lay::CHANNELS, cols = min(p.E - e0, Lay::CHANNELS);
   const int n = clamped_length(p.lengths, b, p.L);
-  const long long row0 = (long long)b * p.L + (p.forward ? 0 : n - 1);   // row of position k: row0 ± k
   const int dir = p.forward ? 1 : -1;
-  const float2 lam = load_vec_pair(p.lam + e0, lane, cols);
-  const float2 rate2 = make_float2(decay_rate(lam.x) * LOG2E, decay_rate(lam.y) * LOG2E);
+  const int span = TILE * (int)blocks;                 // positions of a round
+  const int rounds = n > 0 ? (n - 1) / span + 1 : 0;
+  const int skip = (int)rank * TILE + warp * Lay::WARP_ROWS;   // positions before this warp's in the first round
+  const long long row = (long long)b * p.L + (p.forward ? 0 : n - 1) + (long long)dir * skip;
+  const float2 rate = decay_rates(p.lam + e0, lane, cols), rate2 = __fmul2_rn(rate, two(LOG2E));
+  const float2 k = near_scale(rate2);
+  const bool near = __all_sync(0xffffffffu, rate2.x >= NEAR_RATE2 && rate2.y >= NEAR_RATE2);
   float2 carry = p.h0 ? load_vec_pair(p.h0 + (size_t)b * p.E + e0, lane, cols) : two(0.0f);
 
-  const T* const src[3] = {(const T*)p.x + row0 * p.ldx + e0, (const T*)p.r + row0 * p.ldr + e0,
-                           (const T*)p.g + row0 * p.ldg + e0};
-  const long long step[3] = {dir * p.ldx, dir * p.ldr, dir * p.ldg};
+  RowStream<T, VEC, Lay> xs, rs, gs;
+  xs.start(p.x, row, p.ldx, dir, e0, span, wl);
+  rs.start(p.r, row, p.ldr, dir, e0, span, wl);
+  gs.start(p.g, row, p.ldg, dir, e0, span, wl);
+  const long long out_step = dir * p.ldy, out_leap = span * out_step;
+  T* out = (T*)p.y + row * p.ldy + wl / LANES * FP * out_step + e0 + 2 * lane;
+  const bool wide = VEC && cols == Lay::CHANNELS;
+  constexpr int ARRAY = FG * Lay::GROUP_STRIDE;
+  T* const rows0 = sm.in[0][0] + warp * (32 / LANES) * Lay::GROUP_STRIDE;
   // A position past the end has r = −∞ and x = 0: a = 1, b = 0, and no other
   // test is needed in the arithmetic.
-  auto load = [&](int round) {
-    const long long k0 = ((long long)round * blocks + rank) * TILE;
-    if (k0 < n)
-#pragma unroll
-      for (int i = 0; i < 3; ++i)
-        load_tile<T, VEC, FW * 32>(sm.in[round & 1][i], src[i] + k0 * step[i], step[i], (int)min((long long)TILE, n - k0),
-                                   cols, i == 1 ? -INFINITY : 0.0f);
+  auto load = [&](int buf, int rows) {
+    T* const to = rows0 + buf * 3 * ARRAY;
+    if (wide && rows >= Lay::WARP_ROWS) {
+      xs.whole(to, wl);
+      rs.whole(to + ARRAY, wl);
+      gs.whole(to + 2 * ARRAY, wl);
+    } else if (rows > 0) {
+      copy_part<T, VEC, Lay>(to, xs.at, xs.step, wl, rows, cols, 0.0f);
+      copy_part<T, VEC, Lay>(to + ARRAY, rs.at, rs.step, wl, rows, cols, -INFINITY);
+      copy_part<T, VEC, Lay>(to + 2 * ARRAY, gs.at, gs.step, wl, rows, cols, 0.0f);
+    }
+    xs.at += xs.leap;
+    rs.at += rs.leap;
+    gs.at += gs.leap;
     copies_commit();
   };
 
-  const int rounds = (int)(((long long)n + TILE * blocks - 1) / (TILE * blocks));
-  if (rounds > 0) load(0);
-  if (rounds > 1) load(1);
-  else copies_commit();
+  int left = n - skip;     // positions from this warp's first one to the end
+  load(0, left);
+  load(1, left - span);
   if (blocks > 1) cluster_sync();   // every block of the cluster runs before its shared memory is written
-  for (int round = 0; round < rounds; ++round) {
+  for (int round = 0; round < rounds; ++round, left -= span) {
     const int buf = round & 1;
-    const long long k0 = ((long long)round * blocks + rank) * TILE;
-    const int rows = (int)max(0ll, min((long long)TILE, n - k0));   // of this block's tile
+    const T* const in = rows0 + buf * 3 * ARRAY + wl / LANES * Lay::GROUP_STRIDE;
     copies_wait<1>();
-    __syncthreads();
-    float2 P[FP], H[FP];     // row j's state is P[j] · (state that enters the warp) + H[j]
+    __syncwarp();
+    float2 P[FP], H[FP];     // row j's state is P[j] · (state that enters the group) + H[j]
     float2 a = two(1.0f), h = two(0.0f);
-    const int mine = rows - warp * FP;   // rows of this warp
-    if (mine > 0) {
+    auto compute = [&](auto near_tag) {
 #pragma unroll
       for (int j = 0; j < FP; ++j) {
-        const int at = (warp * FP + j) * STRIP;
-        const float2 x = lane_pair(sm.in[buf][0] + at, lane), r = lane_pair(sm.in[buf][1] + at, lane),
-                     g = lane_pair(sm.in[buf][2] + at, lane);
-        const Gates q = gates2(r, g, rate2);
-        const float2 bx = __fmul2_rn(make_float2(sqrt_approx(q.u.x), sqrt_approx(q.u.y)), __fmul2_rn(q.sg, x));
-        a = __fmul2_rn(a, q.a);
-        h = __ffma2_rn(q.a, h, bx);
+        float2 aj, bj;
+        coefficients<decltype(near_tag)::value>(lane_pair(in + j * Lay::CHANNELS, lane),
+                                                lane_pair(in + ARRAY + j * Lay::CHANNELS, lane),
+                                                lane_pair(in + 2 * ARRAY + j * Lay::CHANNELS, lane), rate2, k, aj, bj);
+        a = j == 0 ? aj : __fmul2_rn(a, aj);
+        h = j == 0 ? bj : __ffma2_rn(aj, h, bj);
         P[j] = a;
         H[j] = h;
       }
+    };
+    if (left > 0) {
+      if (near) compute(std::true_type());
+      else compute(std::false_type());
     }
-    sm.maps[warp][lane] = make_float4(a.x, a.y, h.x, h.y);
-    if (MODE == 2 && mine > 0) {
-      // The group of 64 channels that shares a scale is one row of the warp.
+    float4* const m = maps + buf * nmaps * LANES;   // this lane's in the map of group w: m[w * LANES]
+    if (group < nmaps) m[group * LANES] = make_float4(a.x, a.y, h.x, h.y);
+    if (MODE == 2 && left > 0) {
+      // The channels that share a scale are one row of the warp.
+      const int k0 = n - left;
+      const size_t strip = (size_t)b * strips + e0 / Lay::CHANNELS;
 #pragma unroll
       for (int i = 0; i < 3; ++i) {
-        const size_t tile = ((size_t)b * p.strips + strip) * p.L + k0 + warp * FP;
+        uint16_t* const q = reinterpret_cast<uint16_t*>(p.ck.q[i] + (strip * p.L + k0) * STRIP) + lane;
         uint32_t keep = 0;
 #pragma unroll
         for (int j = 0; j < FP; ++j) {
-          const float2 v = lane_pair(sm.in[buf][i] + (warp * FP + j) * STRIP, lane);
+          const float2 v = lane_pair(in + i * ARRAY + j * STRIP, lane);
           const uint32_t top = __reduce_max_sync(0xffffffffu, max(act8::finite_abs_bits(v.x), act8::finite_abs_bits(v.y)));
           const uint32_t byte = act8::scale_byte(top);
           const float down = act8::scale_down(byte);
           if (lane == j) keep = byte;
-          if (j < mine)
-            reinterpret_cast<uint16_t*>(p.ck.q[i] + (tile + j) * STRIP)[lane] =
-                act8::to_e4m3x2(act8::nan_if_not_finite(v.x) * down, act8::nan_if_not_finite(v.y) * down);
+          if (j < left)
+            q[j * (STRIP / 2)] = act8::to_e4m3x2(act8::nan_if_not_finite(v.x) * down, act8::nan_if_not_finite(v.y) * down);
         }
-        if (lane < FP && lane < mine)
-          p.ck.scales[i][((size_t)b * p.strips + strip) * p.ck.Lp + k0 + warp * FP + lane] = (uint8_t)keep;
+        if (lane < FP && lane < left) p.ck.scales[i][strip * p.ck.Lp + k0 + lane] = (uint8_t)keep;
       }
     }
+    __syncwarp();            // the warp has read its rows: their buffer takes the tile after the next
+    load(buf, left - 2 * span);
     __syncthreads();
-    if (round + 2 < rounds) load(round + 2);
-    else copies_commit();
-    // the value that enters this tile, then this warp
+    // the value that enters this tile, then this group
     float2 enters;
     if (blocks > 1) {
-      float4 tile = sm.maps[0][lane];
+      float4 tile = m[0];
 #pragma unroll
-      for (int w = 1; w < FW; ++w) tile = after(sm.maps[w][lane], tile);
-      enters = through_cluster(box + buf * blocks * 32, tile, warp, FW, lane, rank, blocks, carry);
+      for (int w = 1; w < FG; ++w) tile = after(m[w * LANES], tile);
+      enters = through_cluster(box + buf * blocks * LANES, tile, group, FG, lane, LANES, rank, blocks, carry);
     } else {
-      enters = carry;
-#pragma unroll
-      for (int w = 0; w < FW; ++w) carry = apply(sm.maps[w][lane], carry);
+      enters = round == 0 ? carry : sm.carry[buf ^ 1][lane];
     }
-    if (MODE >= 1 && warp == 0 && rows > 0)
-      reinterpret_cast<float2*>(p.ck.states + ((size_t)b * p.ck.tiles + k0 / TILE) * p.strips * STRIP + e0)[lane] = enters;
+    for (int w = 0; w < group; ++w) enters = apply(m[w * LANES], enters);
+    const int mine = left - wl / LANES * FP;
+    if (MODE >= 1 && group == 0 && mine > 0)
+      reinterpret_cast<float2*>(p.ck.states + ((size_t)b * p.ck.tiles + (n - mine) / TILE) * p.strips * STRIP + e0)[lane] = enters;
+    if (blocks == 1 && group == FG - 1) {
+      carry = apply(make_float4(a.x, a.y, h.x, h.y), enters);
+      sm.carry[buf][lane] = carry;
+    }
+    if (wide && left >= Lay::WARP_ROWS) {
 #pragma unroll
-    for (int w = 0; w < FW - 1; ++w)
-      if (w < warp) enters = apply(sm.maps[w][lane], enters);
-    T* out = (T*)p.y + (row0 + dir * (k0 + warp * FP)) * p.ldy + e0;
+      for (int j = 0; j < FP; ++j) store_whole_pair(out + j * out_step, __ffma2_rn(P[j], enters, H[j]));
+    } else {
 #pragma unroll
-    for (int j = 0; j < FP; ++j)
-      if (j < mine) store_pair<VEC>(out + j * dir * p.ldy, lane, cols, __ffma2_rn(P[j], enters, H[j]));
+      for (int j = 0; j < FP; ++j)
+        if (j < mine) store_pair<VEC>(out + j * out_step - 2 * lane, lane, cols, __ffma2_rn(P[j], enters, H[j]));
+    }
+    out += out_leap;
   }
-  if (p.h_last && rank == 0 && warp == 0) store_pair<false>(p.h_last + (size_t)b * p.E + e0, lane, cols, carry);
+  if (p.h_last && rank == 0 && group == FG - 1) store_pair<false>(p.h_last + (size_t)b * p.E + e0, lane, cols, carry);
 }
 
 // A few positions (a step of decoding): a thread walks its two channels.
@@ -408,15 +539,14 @@ __global__ void __launch_bounds__(128) gated_walk_kernel(const FwdArgs p) {
   const int b = (int)(at / pairs), pair = (int)(at % pairs);
   if (b >= p.B) return;
   const int n = clamped_length(p.lengths, b, p.L);
-  const float2 lam = load_vec_pair(p.lam, pair, p.E);
-  const float2 rate2 = make_float2(decay_rate(lam.x) * LOG2E, decay_rate(lam.y) * LOG2E);
+  const float2 rate2 = __fmul2_rn(decay_rates(p.lam, pair, p.E), two(LOG2E));
   float2 h = p.h0 ? load_vec_pair(p.h0 + (size_t)b * p.E, pair, p.E) : two(0.0f);
   for (int k = 0; k < n; ++k) {
     const long long m = (long long)b * p.L + (p.forward ? k : n - 1 - k);
-    const Gates q = gates2(load_pair<VEC>((const T*)p.r + m * p.ldr, pair, p.E),
-                           load_pair<VEC>((const T*)p.g + m * p.ldg, pair, p.E), rate2);
-    const float2 x = load_pair<VEC>((const T*)p.x + m * p.ldx, pair, p.E);
-    h = __ffma2_rn(q.a, h, __fmul2_rn(make_float2(sqrt_approx(q.u.x), sqrt_approx(q.u.y)), __fmul2_rn(q.sg, x)));
+    float2 aj, bj;
+    coefficients<false>(load_pair<VEC>((const T*)p.x + m * p.ldx, pair, p.E), load_pair<VEC>((const T*)p.r + m * p.ldr, pair, p.E),
+                        load_pair<VEC>((const T*)p.g + m * p.ldg, pair, p.E), rate2, two(0.0f), aj, bj);
+    h = __ffma2_rn(aj, h, bj);
     store_pair<VEC>((T*)p.y + m * p.ldy, pair, p.E, h);
   }
   if (p.h_last) store_pair<false>(p.h_last + (size_t)b * p.E, pair, p.E, h);

@@ -227,6 +227,30 @@ def test_gradient_from_8_bits(B, L, E, lens, forward, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("spread", ["all", "some", "border"])
+def test_fast_and_slow_channels(spread, dtype):
+    """Decays from none to all at once in every channel, in a few channels of a row, and around half the state kept."""
+    B, L, E, lens = 3, 200, 200, [200, 77, 130]
+    d = make(B, L, E, dtype, seed=4, lens=lens)
+    gen = torch.Generator().manual_seed(44)
+    if spread == "all":
+        d["lam"] = torch.randn(E, generator=gen) * 4
+    elif spread == "some":
+        d["lam"][::70] = torch.randn(len(range(0, E, 70)), generator=gen) * 2
+    else:                                          # 8 softplus(lam) log2 e from 0.2 to 1.2
+        sp = torch.linspace(0.2, 1.2, E, dtype=torch.float64) / (8 * 1.4426950408889634)
+        d["lam"] = torch.log(torch.expm1(sp)).float()
+    c = dev(d)
+    for forward in (False, True):
+        y, h, _, out = train(d, c, B, L, E, dtype, forward, False)
+        check_forward(d, y, h, B, L, forward)
+        check_backward(d, out, B, L, forward)
+    y, h = bd.gated_scan(c["x"], c["r"], c["g"], c["lam"], bd.gated_dims(E, dtype), B, L, h0=c["h0"],
+                         lengths=lengths_tensor(d, L))
+    check_forward(d, y, h, B, L, False)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
 def test_columns_of_wider_arrays(dtype):
     """x, r and g as columns of one projection's output, y and the gradients as columns too: once at offsets that keep
     rows on 16-byte boundaries, once at odd ones."""
