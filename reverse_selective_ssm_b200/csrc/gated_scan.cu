@@ -125,12 +125,15 @@ Ckpt checkpoint_at(const CkptPlan& k, void* base) {
   return ck;
 }
 
-// Blocks of a cluster that share a sequence's 64 channels.
-uint32_t cluster_blocks(int B, int strips, int L, int slots) {
+// Blocks of a cluster that share a sequence's channels, and warps of a block.
+struct Split {
+  uint32_t blocks;
+  int warps;
+};
+Split split(long long jobs, int L, int small, int large, int resident) {
   const int tiles = (L - 1) / TILE + 1;
-  uint32_t c = 1;
-  while (c < MAX_CLUSTER && 2 * c <= (uint32_t)tiles && (long long)B * strips * c < slots) c *= 2;
-  return c;
+  Split s{1, small};
+  return s;
 }
 
 template <typename Args>
@@ -173,24 +176,29 @@ r2l_status run_forward(const FwdArgs& p, int mode, cudaStream_t st) {
     R2L_LAUNCH_CHECK();
     return R2L_OK;
   }
-  const int strips32 = (p.E - 1) / 32 + 1;
   if (mode == 2) {
-    const uint32_t c = cluster_blocks(p.B, p.strips, p.L, 148 * (sizeof(T) == 2 ? 3 : 2));
-    return launch(gated_scan_kernel<T, VEC, 2, 32>, p, (long long)p.B * p.strips, c, FG * 32, fwd_smem_bytes<T, 32>(c), st);
+    const long long jobs = (long long)p.B * p.strips;
+    const Split c = split(jobs, p.L, 8, 32, 0);
+    return launch(gated_scan_kernel<T, VEC, 2, 32, 8>, p, jobs, c.blocks, 256, fwd_smem_bytes<T, 32, 8>(c.blocks), st);
   }
-  const uint32_t c = cluster_blocks(p.B, strips32, p.L, 148 * (sizeof(T) == 2 ? 7 : 4));
-  return launch(mode == 0 ? gated_scan_kernel<T, VEC, 0, 16> : gated_scan_kernel<T, VEC, 1, 16>, p, (long long)p.B * strips32,
-                c, FG * 16, fwd_smem_bytes<T, 16>(c), st);
+  const long long jobs = (long long)p.B * ((p.E - 1) / 32 + 1);
+  const Split c = split(jobs, p.L, 4, 16, 0);
+  if (sizeof(T) == 4 || c.warps == 4)
+    return launch(mode == 0 ? gated_scan_kernel<T, VEC, 0, 16, 4> : gated_scan_kernel<T, VEC, 1, 16, 4>, p, jobs, c.blocks, 128,
+                  fwd_smem_bytes<T, 16, 4>(c.blocks), st);
+  return launch(mode == 0 ? gated_scan_kernel<T, VEC, 0, 16, 16> : gated_scan_kernel<T, VEC, 1, 16, 16>, p, jobs, c.blocks, 512,
+                fwd_smem_bytes<T, 16, 16>(c.blocks), st);
 }
 
-uint32_t backward_blocks(const r2l_dims* d, int B, int L) {
-  return cluster_blocks(B, (d->d_inner - 1) / GROUP + 1, L, 148 * (d->dtype == R2L_BF16 ? 2 : 1));
+Split backward_split(const r2l_dims* d, int B, int L) {
+  return split((long long)B * ((d->d_inner - 1) / 32 + 1), L, 4, 16, 0);
 }
 
 template <typename T, bool VEC, bool ACT8>
-r2l_status run_backward(const BwdArgs& p, uint32_t c, cudaStream_t st) {
+r2l_status run_backward(const BwdArgs& p, Split c, cudaStream_t st) {
   using namespace r2l::gated;
-  return launch(gated_bwd_kernel<T, VEC, ACT8>, p, (long long)p.B * p.strips, c, BW * 32, sizeof(BwdSmem<T, ACT8>) + box_bytes(c), st);
+  const long long jobs = (long long)p.B * ((p.E - 1) / 32 + 1);
+  return launch(gated_bwd_kernel<T, VEC, ACT8, 4>, p, jobs, c.blocks, 128, bwd_smem_bytes<T, ACT8, 4>(c.blocks), st);
 }
 
 // Rows of E elements of `size` bytes with stride ld.
@@ -255,7 +263,7 @@ r2l_status forward_impl(const r2l_gated_in* in, void* y, int ldy, float* h_last,
 
 // Shares of dlam, one row for each block of channels' blocks.
 size_t part_bytes(const r2l_dims* d, int B, int L) {
-  return (size_t)B * backward_blocks(d, B, L) * align_up(d->d_inner, GROUP) * sizeof(float);
+  return (size_t)B * backward_split(d, B, L).blocks * align_up(d->d_inner, GROUP) * sizeof(float);
 }
 
 }  // namespace
@@ -329,7 +337,7 @@ r2l_status r2l_gated_scan_backward(const r2l_gated_in* in, const void* dy, int l
   const bool vec = (act8 || (rows16(p.x, p.ldx, es) && rows16(p.r, p.ldr, es) && rows16(p.g, p.ldg, es))) &&
                    rows16(p.dy, p.ld_dy, es) && rows16(p.dx, p.ld_dx, es) && rows16(p.dr, p.ld_dr, es) &&
                    rows16(p.dg, p.ld_dg, es);
-  const uint32_t c = backward_blocks(dims, B, L);
+  const Split c = backward_split(dims, B, L);
   cudaStream_t st = (cudaStream_t)stream;
   if (dims->dtype == R2L_BF16) {
     if (act8) R2L_TRY((vec ? run_backward<bf16, true, true> : run_backward<bf16, false, true>)(p, c, st));
@@ -338,7 +346,7 @@ r2l_status r2l_gated_scan_backward(const r2l_gated_in* in, const void* dy, int l
     if (act8) R2L_TRY((vec ? run_backward<float, true, true> : run_backward<float, false, true>)(p, c, st));
     else R2L_TRY((vec ? run_backward<float, true, false> : run_backward<float, false, false>)(p, c, st));
   }
-  r2l::gated::gated_dlam_kernel<<<(E + 31) / 32, 256, 0, st>>>(p.part, (int)(B * c), p.strips * GROUP, p.lam, E, grads->dlam);
+  r2l::gated::gated_dlam_kernel<<<(E + 31) / 32, 256, 0, st>>>(p.part, (int)(B * c.blocks), p.strips * GROUP, p.lam, E, grads->dlam);
   R2L_LAUNCH_CHECK();
   return R2L_OK;
 }

@@ -217,13 +217,17 @@ __device__ __forceinline__ uint32_t bits_twice<bf16>(float v) {
 template <typename T, int LANES, int ROWS>
 struct Layout {
   static constexpr int CHANNELS = 2 * LANES;
-  static constexpr int GROUP_STRIDE = ROWS * CHANNELS + (LANES < 32 ? 64 / (int)sizeof(T) : 0);   // elements
+  static constexpr int GROUPS = 32 / LANES;                  // of a warp
+  static constexpr int GROUP_STRIDE = ROWS * CHANNELS + (GROUPS > 1 ? 64 / (int)sizeof(T) : 0);   // elements
+  static constexpr int WARP_STRIDE = GROUPS * GROUP_STRIDE;
   static constexpr int PER = 16 / (int)sizeof(T);            // elements of a copy
   static constexpr int CHUNKS = CHANNELS / PER;              // copies of a row
   static constexpr int AT_ONCE = 32 / CHUNKS;                // rows that a warp's lanes copy at once
-  static constexpr int WARP_ROWS = ROWS * (32 / LANES);
-  static_assert(ROWS % AT_ONCE == 0, "a copy of the warp's lanes stays within a group");
+  static constexpr int WARP_ROWS = ROWS * GROUPS;
+  static_assert(ROWS % AT_ONCE == 0 || AT_ONCE == WARP_ROWS, "at(i + j) = at(i) + at(j) for the rows of a copy");
   static __device__ __forceinline__ int at(int row) { return row / ROWS * GROUP_STRIDE + row % ROWS * CHANNELS; }
+  // This lane's chunk of the first rows that are copied at once.
+  static __device__ __forceinline__ int chunk(int wl) { return at(wl / CHUNKS) + wl % CHUNKS * PER; }
 };
 
 // The rows of one warp on their way to shared memory.  A warp copies only the
@@ -241,7 +245,7 @@ struct RowStream {
   }
   // The next tile's rows into dst.
   __device__ __forceinline__ void whole(T* dst, int lane) const {
-    dst += lane * LAY::PER;    // chunk `lane` of AT_ONCE whole rows
+    dst += LAY::chunk(lane);
 #pragma unroll
     for (int i = 0; i < LAY::WARP_ROWS; i += LAY::AT_ONCE) copy16(dst + LAY::at(i), at + i * step, 16);
   }
@@ -260,7 +264,7 @@ __device__ __noinline__ void copy_part(T* dst, const T* at, long long step, int 
   if (VEC) {
     const int c = lane % LAY::CHUNKS * LAY::PER, bytes = min(max(cols - c, 0), LAY::PER) * (int)sizeof(T);
     for (int i = 0; i < LAY::WARP_ROWS; i += LAY::AT_ONCE) {
-      T* const to = dst + lane * LAY::PER + LAY::at(i);
+      T* const to = dst + LAY::chunk(lane) + LAY::at(i);
       if (lane / LAY::CHUNKS + i < rows) {
         copy16(to, bytes ? at + i * step : at - c, bytes);
       } else {
@@ -354,53 +358,58 @@ __device__ __forceinline__ float4 after(float4 second, float4 first) {
 // The tiles' maps of one round through the cluster: `mine` is this block's, and
 // `carry` the value that enters the first block's tile; returns the value that
 // enters this block's and moves carry past the last block's.  box holds
-// [blocks][lanes] maps and alternates between two buffers from round to
-// round: a block writes a buffer again only after the barrier of the round
-// between, which every reader of the buffer has passed.
-__device__ __forceinline__ float2 through_cluster(float4* box, float4 mine, int group, int groups, int lane, int lanes,
-                                                  uint32_t rank, uint32_t blocks, float2& carry) {
-  for (uint32_t to = group; to < blocks; to += groups) store_to_rank(box + rank * lanes + lane, to, mine);
+// [blocks][LANES] maps and alternates between two buffers from round to round:
+// a block writes a buffer again only after the barrier of the round between,
+// which every reader of the buffer has passed.
+template <int LANES>
+__device__ __forceinline__ float2 through_cluster(float4* box, float4 mine, int group, int groups, int lane, uint32_t rank,
+                                                  uint32_t blocks, float2& carry) {
+  for (uint32_t to = group; to < blocks; to += groups) store_to_rank(box + rank * LANES + lane, to, mine);
+  __syncwarp();
   cluster_sync();
   float2 enters = carry;
   for (uint32_t q = 0; q < blocks; ++q) {
     if (q == rank) enters = carry;
-    carry = apply(box[q * lanes + lane], carry);
+    carry = apply(box[q * LANES + lane], carry);
   }
   return enters;
 }
 
+// The other half warp's value.
+__device__ __forceinline__ float2 other_half(float2 v) {
+  return make_float2(__shfl_xor_sync(0xffffffffu, v.x, 16), __shfl_xor_sync(0xffffffffu, v.y, 16));
+}
+
 // ---------------------------------------------------------------- forward
 
-constexpr int FG = 8;              // groups of rows of a forward block
-constexpr int FP = TILE / FG;      // rows of a group
+constexpr int ROWS = 8;      // consecutive rows of a thread
 
-// In shared memory, behind it the maps of the block's groups, [2][maps][LANES],
-// and of the cluster's blocks, [2][blocks][LANES].  A block by itself has no use
-// for its last group's map.
-template <typename T, int LANES>
+// In shared memory, behind it the maps of the block's warps, [2][WARPS][LANES],
+// and of the cluster's blocks, [2][blocks][LANES].
+template <typename T, int LANES, int WARPS>
 struct FwdSmem {
-  T in[2][3][FG * Layout<T, LANES, FP>::GROUP_STRIDE];
+  T in[2][3][WARPS * Layout<T, LANES, ROWS>::WARP_STRIDE];
+  float4 maps[2][WARPS][LANES];
   float2 carry[2][LANES];
 };
-__host__ __device__ constexpr int group_maps(uint32_t blocks) { return blocks > 1 ? FG : FG - 1; }
-template <typename T, int LANES>
+template <typename T, int LANES, int WARPS>
 constexpr size_t fwd_smem_bytes(uint32_t blocks) {
-  return sizeof(FwdSmem<T, LANES>) + 2 * sizeof(float4) * LANES * (group_maps(blocks) + (blocks > 1 ? blocks : 0));
+  return sizeof(FwdSmem<T, LANES, WARPS>) + (blocks > 1 ? 2 * sizeof(float4) * LANES * blocks : 0);
 }
 
 // MODE 0: the recurrence; 1: also the states of a checkpoint; 2: and its 8 bits.
-template <typename T, bool VEC, int MODE, int LANES>
-__global__ void __launch_bounds__(FG * LANES, (sizeof(T) == 2 ? 7 : 4) * 32 / LANES / 2)
+template <typename T, bool VEC, int MODE, int LANES, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, (sizeof(T) == 2 ? (WARPS == 16 ? 32 : LANES == 16 ? 28 : 24) : 16) / WARPS)
     gated_scan_kernel(const FwdArgs p, const uint32_t blocks) {
-  typedef Layout<T, LANES, FP> Lay;
+  typedef Layout<T, LANES, ROWS> Lay;
+  typedef FwdSmem<T, LANES, WARPS> Smem;
   static_assert(MODE < 2 || LANES == 32, "the channels of a scale are a row of the warp");
+  constexpr int SPAN = WARPS * Lay::WARP_ROWS;      // rows of the block's tile
   extern __shared__ __align__(16) unsigned char smem_raw[];
-  FwdSmem<T, LANES>& sm = *reinterpret_cast<FwdSmem<T, LANES>*>(smem_raw);
+  Smem& sm = *reinterpret_cast<Smem*>(smem_raw);
+  float4* const box = reinterpret_cast<float4*>(smem_raw + sizeof(Smem));
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0), wl = threadIdx.x & 31;   // uniform for the compiler too
-  const int lane = wl % LANES, group = warp * (32 / LANES) + wl / LANES;
-  const int nmaps = group_maps(blocks);
-  float4* const maps = reinterpret_cast<float4*>(smem_raw + sizeof(FwdSmem<T, LANES>)) + lane;
-  float4* const box = reinterpret_cast<float4*>(smem_raw + sizeof(FwdSmem<T, LANES>)) + 2 * nmaps * LANES;
+  const int lane = wl % LANES, half = wl / LANES;
   if (p.status && blockIdx.x == 0) write_status(p.lengths, p.B, p.L, p.status);
   const uint32_t rank = blockIdx.x % blocks;
   const uint32_t job = blockIdx.x / blocks;
@@ -408,11 +417,11 @@ __global__ void __launch_bounds__(FG * LANES, (sizeof(T) == 2 ? 7 : 4) * 32 / LA
   const int b = (int)(job / strips), e0 = (int)(job % strips) * Lay::CHANNELS, cols = min(p.E - e0, Lay::CHANNELS);
   const int n = clamped_length(p.lengths, b, p.L);
   const int dir = p.forward ? 1 : -1;
-  const int span = TILE * (int)blocks;                 // positions of a round
+  const int span = SPAN * (int)blocks;                 // positions of a round
   const int rounds = n > 0 ? (n - 1) / span + 1 : 0;
-  const int skip = (int)rank * TILE + warp * Lay::WARP_ROWS;   // positions before this warp's in the first round
+  const int skip = (int)rank * SPAN + warp * Lay::WARP_ROWS;   // positions before this warp's in the first round
   const long long row = (long long)b * p.L + (p.forward ? 0 : n - 1) + (long long)dir * skip;
-  const float2 rate = decay_rates(p.lam + e0, lane, cols), rate2 = __fmul2_rn(rate, two(LOG2E));
+  const float2 rate2 = __fmul2_rn(decay_rates(p.lam + e0, lane, cols), two(LOG2E));
   const float2 k = near_scale(rate2);
   const bool near = __all_sync(0xffffffffu, rate2.x >= NEAR_RATE2 && rate2.y >= NEAR_RATE2);
   float2 carry = p.h0 ? load_vec_pair(p.h0 + (size_t)b * p.E + e0, lane, cols) : two(0.0f);
@@ -422,10 +431,10 @@ __global__ void __launch_bounds__(FG * LANES, (sizeof(T) == 2 ? 7 : 4) * 32 / LA
   rs.start(p.r, row, p.ldr, dir, e0, span, wl);
   gs.start(p.g, row, p.ldg, dir, e0, span, wl);
   const long long out_step = dir * p.ldy, out_leap = span * out_step;
-  T* out = (T*)p.y + row * p.ldy + wl / LANES * FP * out_step + e0 + 2 * lane;
+  T* out = (T*)p.y + row * p.ldy + half * ROWS * out_step + e0 + 2 * lane;
   const bool wide = VEC && cols == Lay::CHANNELS;
-  constexpr int ARRAY = FG * Lay::GROUP_STRIDE;
-  T* const rows0 = sm.in[0][0] + warp * (32 / LANES) * Lay::GROUP_STRIDE;
+  constexpr int ARRAY = WARPS * Lay::WARP_STRIDE;
+  T* const rows0 = sm.in[0][0] + warp * Lay::WARP_STRIDE;
   // A position past the end has r = −∞ and x = 0: a = 1, b = 0, and no other
   // test is needed in the arithmetic.
   auto load = [&](int buf, int rows) {
@@ -451,14 +460,14 @@ __global__ void __launch_bounds__(FG * LANES, (sizeof(T) == 2 ? 7 : 4) * 32 / LA
   if (blocks > 1) cluster_sync();   // every block of the cluster runs before its shared memory is written
   for (int round = 0; round < rounds; ++round, left -= span) {
     const int buf = round & 1;
-    const T* const in = rows0 + buf * 3 * ARRAY + wl / LANES * Lay::GROUP_STRIDE;
+    const T* const in = rows0 + buf * 3 * ARRAY + half * Lay::GROUP_STRIDE;
     copies_wait<1>();
     __syncwarp();
-    float2 P[FP], H[FP];     // row j's state is P[j] · (state that enters the group) + H[j]
+    float2 P[ROWS], H[ROWS];     // row j's state is P[j] · (state that enters the group) + H[j]
     float2 a = two(1.0f), h = two(0.0f);
     auto compute = [&](auto near_tag) {
 #pragma unroll
-      for (int j = 0; j < FP; ++j) {
+      for (int j = 0; j < ROWS; ++j) {
         float2 aj, bj;
         coefficients<decltype(near_tag)::value>(lane_pair(in + j * Lay::CHANNELS, lane),
                                                 lane_pair(in + ARRAY + j * Lay::CHANNELS, lane),
@@ -473,8 +482,15 @@ __global__ void __launch_bounds__(FG * LANES, (sizeof(T) == 2 ? 7 : 4) * 32 / LA
       if (near) compute(std::true_type());
       else compute(std::false_type());
     }
-    float4* const m = maps + buf * nmaps * LANES;   // this lane's in the map of group w: m[w * LANES]
-    if (group < nmaps) m[group * LANES] = make_float4(a.x, a.y, h.x, h.y);
+    // the warp's map, and what its first half's does to the second half
+    float4 map = make_float4(a.x, a.y, h.x, h.y), before = make_float4(1.0f, 1.0f, 0.0f, 0.0f);
+    if (Lay::GROUPS == 2) {
+      const float2 oa = other_half(a), oh = other_half(h);
+      const float4 o = make_float4(oa.x, oa.y, oh.x, oh.y);
+      if (half) before = o;
+      map = after(half ? map : o, half ? o : map);
+    }
+    if (half == 0) sm.maps[buf][warp][lane] = map;
     if (MODE == 2 && left > 0) {
       // The channels that share a scale are one row of the warp.
       const int k0 = n - left;
@@ -484,7 +500,7 @@ __global__ void __launch_bounds__(FG * LANES, (sizeof(T) == 2 ? 7 : 4) * 32 / LA
         uint16_t* const q = reinterpret_cast<uint16_t*>(p.ck.q[i] + (strip * p.L + k0) * STRIP) + lane;
         uint32_t keep = 0;
 #pragma unroll
-        for (int j = 0; j < FP; ++j) {
+        for (int j = 0; j < ROWS; ++j) {
           const float2 v = lane_pair(in + i * ARRAY + j * STRIP, lane);
           const uint32_t top = __reduce_max_sync(0xffffffffu, max(act8::finite_abs_bits(v.x), act8::finite_abs_bits(v.y)));
           const uint32_t byte = act8::scale_byte(top);
@@ -493,41 +509,44 @@ __global__ void __launch_bounds__(FG * LANES, (sizeof(T) == 2 ? 7 : 4) * 32 / LA
           if (j < left)
             q[j * (STRIP / 2)] = act8::to_e4m3x2(act8::nan_if_not_finite(v.x) * down, act8::nan_if_not_finite(v.y) * down);
         }
-        if (lane < FP && lane < left) p.ck.scales[i][strip * p.ck.Lp + k0 + lane] = (uint8_t)keep;
+        if (lane < ROWS && lane < left) p.ck.scales[i][strip * p.ck.Lp + k0 + lane] = (uint8_t)keep;
       }
     }
     __syncwarp();            // the warp has read its rows: their buffer takes the tile after the next
     load(buf, left - 2 * span);
     __syncthreads();
-    // the value that enters this tile, then this group
+    // the value that enters this tile, this warp, this group
     float2 enters;
     if (blocks > 1) {
-      float4 tile = m[0];
+      float4 tile = sm.maps[buf][0][lane];
 #pragma unroll
-      for (int w = 1; w < FG; ++w) tile = after(m[w * LANES], tile);
-      enters = through_cluster(box + buf * blocks * LANES, tile, group, FG, lane, LANES, rank, blocks, carry);
+      for (int w = 1; w < WARPS; ++w) tile = after(sm.maps[buf][w][lane], tile);
+      enters = through_cluster<LANES>(box + buf * blocks * LANES, tile, warp * Lay::GROUPS + half, WARPS * Lay::GROUPS, lane,
+                                      rank, blocks, carry);
     } else {
       enters = round == 0 ? carry : sm.carry[buf ^ 1][lane];
     }
-    for (int w = 0; w < group; ++w) enters = apply(m[w * LANES], enters);
-    const int mine = left - wl / LANES * FP;
-    if (MODE >= 1 && group == 0 && mine > 0)
-      reinterpret_cast<float2*>(p.ck.states + ((size_t)b * p.ck.tiles + (n - mine) / TILE) * p.strips * STRIP + e0)[lane] = enters;
-    if (blocks == 1 && group == FG - 1) {
-      carry = apply(make_float4(a.x, a.y, h.x, h.y), enters);
-      sm.carry[buf][lane] = carry;
+    for (int w = 0; w < warp; ++w) enters = apply(sm.maps[buf][w][lane], enters);
+    if (blocks == 1 && warp == WARPS - 1) {
+      carry = apply(map, enters);
+      if (half == 0) sm.carry[buf][lane] = carry;
     }
+    if (MODE >= 1 && warp % (TILE / Lay::WARP_ROWS) == 0 && half == 0 && left > 0)
+      reinterpret_cast<float2*>(p.ck.states + ((size_t)b * p.ck.tiles + (n - left) / TILE) * p.strips * STRIP + e0)[lane] = enters;
+    if (Lay::GROUPS == 2) enters = apply(before, enters);
     if (wide && left >= Lay::WARP_ROWS) {
 #pragma unroll
-      for (int j = 0; j < FP; ++j) store_whole_pair(out + j * out_step, __ffma2_rn(P[j], enters, H[j]));
+      for (int j = 0; j < ROWS; ++j) store_whole_pair(out + j * out_step, __ffma2_rn(P[j], enters, H[j]));
     } else {
+      const int mine = left - half * ROWS;
 #pragma unroll
-      for (int j = 0; j < FP; ++j)
+      for (int j = 0; j < ROWS; ++j)
         if (j < mine) store_pair<VEC>(out + j * out_step - 2 * lane, lane, cols, __ffma2_rn(P[j], enters, H[j]));
     }
     out += out_leap;
   }
-  if (p.h_last && rank == 0 && group == FG - 1) store_pair<false>(p.h_last + (size_t)b * p.E + e0, lane, cols, carry);
+  if (p.h_last && rank == 0 && warp == WARPS - 1 && half == 0)
+    store_pair<false>(p.h_last + (size_t)b * p.E + e0, lane, cols, carry);
 }
 
 // A few positions (a step of decoding): a thread walks its two channels.
