@@ -39,7 +39,7 @@ __device__ __forceinline__ float2 near_beta_inverse(float2 l2) {
 }
 
 template <typename T, bool VEC, bool ACT8, int WARPS>
-__global__ void __launch_bounds__(WARPS * 32, (sizeof(T) == 2 ? 16 : 12) / WARPS)
+__global__ void __launch_bounds__(WARPS * 32, (sizeof(T) == 2 || WARPS == 8 ? 16 : 12) / WARPS)
     gated_bwd_kernel(const BwdArgs p, const uint32_t blocks) {
   typedef BwdSmem<T, ACT8, WARPS> Smem;
   typedef typename Smem::Q Q;
@@ -60,99 +60,76 @@ __global__ void __launch_bounds__(WARPS * 32, (sizeof(T) == 2 ? 16 : 12) / WARPS
   const int dir = p.forward ? 1 : -1;
   const int span = SPAN * (int)blocks;
   const int rounds = n > 0 ? (n - 1) / span + 1 : 0;
-  // position of this warp's first row in the first round: the last round of the forward, its blocks in reverse
-  const long long k0 = (long long)(rounds - 1) * span + (long long)(blocks - 1 - rank) * SPAN + warp * Lay::WARP_ROWS;
-  const long long row = (long long)b * p.L + (p.forward ? 0 : n - 1) + dir * k0;
-  const float2 rate = decay_rates(p.lam + e0, lane, cols), rate2 = __fmul2_rn(rate, two(LOG2E));
-  const float2 k = near_scale(rate2);
-  const float2 nik = make_float2(k.x > 0.0f ? -1.0f / k.x : 0.0f, k.y > 0.0f ? -1.0f / k.y : 0.0f);
-  const bool near = __all_sync(0xffffffffu, rate2.x >= NEAR_RATE2 && rate2.y >= NEAR_RATE2);
-  float2 carry = p.dh_last ? load_vec_pair(p.dh_last + (size_t)b * p.E + e0, lane, cols) : two(0.0f);
-  float2 dlam = two(0.0f);
-
-  RowStream<Q, true, LayQ> q0, q1, q2;             // x, r, g of a checkpoint: rows of 64 bytes in scan order
-  RowStream<T, VEC, Lay> xs, rs, gs, ds;
+  // this warp's first position in the first round: the last round of the forward, its blocks in reverse
+  const int k0 = (rounds - 1) * span + (int)(blocks - 1 - rank) * SPAN + warp * Lay::WARP_ROWS;
+  const long long row0 = (long long)b * p.L + (p.forward ? 0 : n - 1);   // position 0
   const size_t strip = (size_t)b * p.strips + e0 / STRIP;
-  if (ACT8) {
-    q0.start(p.ck.q[0], (long long)strip * p.L + k0, STRIP, 1, e0 % STRIP, -span, wl);
-    q1.start(p.ck.q[1], (long long)strip * p.L + k0, STRIP, 1, e0 % STRIP, -span, wl);
-    q2.start(p.ck.q[2], (long long)strip * p.L + k0, STRIP, 1, e0 % STRIP, -span, wl);
+  const Q* in0[3];          // x, r, g: position 0
+  int in_step[3];
+  if constexpr (ACT8) {     // rows of 64 bytes in scan order
+#pragma unroll
+    for (int i = 0; i < 3; ++i) in0[i] = p.ck.q[i] + strip * p.L * STRIP + e0 % STRIP, in_step[i] = STRIP;
   } else {
-    xs.start(p.x, row, p.ldx, dir, e0, -span, wl);
-    rs.start(p.r, row, p.ldr, dir, e0, -span, wl);
-    gs.start(p.g, row, p.ldg, dir, e0, -span, wl);
+    in0[0] = (const T*)p.x + row0 * p.ldx + e0, in_step[0] = dir * (int)p.ldx;
+    in0[1] = (const T*)p.r + row0 * p.ldr + e0, in_step[1] = dir * (int)p.ldr;
+    in0[2] = (const T*)p.g + row0 * p.ldg + e0, in_step[2] = dir * (int)p.ldg;
   }
-  ds.start(p.dy, row, p.ld_dy, dir, e0, -span, wl);
-  const long long dx_step = dir * p.ld_dx, dr_step = dir * p.ld_dr, dg_step = dir * p.ld_dg;
-  T* dx = (T*)p.dx + row * p.ld_dx + half * ROWS * dx_step + e0 + 2 * lane;
-  T* dr = (T*)p.dr + row * p.ld_dr + half * ROWS * dr_step + e0 + 2 * lane;
-  T* dg = (T*)p.dg + row * p.ld_dg + half * ROWS * dg_step + e0 + 2 * lane;
-  const bool wide = VEC && cols == Lay::CHANNELS;
+  const T* const first_dy = (const T*)p.dy + row0 * p.ld_dy + e0;
+  T* const dx0 = (T*)p.dx + row0 * p.ld_dx + e0;
+  T* const dr0 = (T*)p.dr + row0 * p.ld_dr + e0;
+  T* const dg0 = (T*)p.dg + row0 * p.ld_dg + e0;
+  const float* const states0 = p.ck.states + (long long)b * p.ck.tiles * p.strips * STRIP + e0;
+  const int dy_step = dir * (int)p.ld_dy, dx_step = dir * (int)p.ld_dx, dr_step = dir * (int)p.ld_dr, dg_step = dir * (int)p.ld_dg;
   constexpr int ARRAY = WARPS * LayQ::WARP_STRIDE, DY = WARPS * Lay::WARP_STRIDE;
   Q* const rows0 = sm.in[0][0] + warp * LayQ::WARP_STRIDE;
   T* const dy0 = sm.dy[0] + warp * Lay::WARP_STRIDE;
-  long long kload = k0;      // position of the next rows to load
-  auto load = [&](int buf) {
-    const int rows = (int)min((long long)Lay::WARP_ROWS, n - kload);
-    if (kload >= 0 && rows > 0) {
+
+  const bool wide = VEC && cols == Lay::CHANNELS;
+  auto load = [&](auto wide_tag, int buf, int k) {
+    constexpr bool WIDE = decltype(wide_tag)::value;
+    if (k >= 0 && k < n) {
       Q* const to = rows0 + buf * 3 * ARRAY;
-      if (ACT8) {
-        if (wl / LayQ::CHUNKS < rows) {
-          q0.whole(to, wl);
-          q1.whole(to + ARRAY, wl);
-          q2.whole(to + 2 * ARRAY, wl);
-        }
-        if (wl < 3) copy16(sm.scales[buf][warp][wl], p.ck.scales[wl] + strip * p.ck.Lp + kload, 16);
-      } else if (wide && rows == Lay::WARP_ROWS) {
-        xs.whole((T*)to, wl);
-        rs.whole((T*)to + ARRAY, wl);
-        gs.whole((T*)to + 2 * ARRAY, wl);
-      } else {
-        copy_part<T, VEC, Lay>((T*)to, xs.at, xs.step, wl, rows, cols, 0.0f);
-        copy_part<T, VEC, Lay>((T*)to + ARRAY, rs.at, rs.step, wl, rows, cols, -INFINITY);
-        copy_part<T, VEC, Lay>((T*)to + 2 * ARRAY, gs.at, gs.step, wl, rows, cols, 0.0f);
-      }
-      if (wide && rows == Lay::WARP_ROWS) ds.whole(dy0 + buf * DY, wl);
-      else copy_part<T, VEC, Lay>(dy0 + buf * DY, ds.at, ds.step, wl, rows, cols, 0.0f);
-      if (wl < BL / 2)
-        copy16(sm.states[buf][warp] + 4 * wl, p.ck.states + ((size_t)b * p.ck.tiles + kload / TILE) * p.strips * STRIP + e0 + 4 * wl, 16);
+#pragma unroll
+      for (int i = 0; i < 3; ++i) copy_rows<Q, WIDE || ACT8, LayQ>(to + i * ARRAY, in0[i], in_step[i], k, n, cols, wl);
+      copy_rows<T, WIDE, Lay>(dy0 + buf * DY, first_dy, dy_step, k, n, cols, wl);
+      if (wl < BL / 2) copy16(sm.states[buf][warp] + 4 * wl, states0 + (long long)(k / TILE) * (p.strips * STRIP) + 4 * wl, 16);
+      if (ACT8 && wl < 3) copy16(sm.scales[buf][warp][wl], p.ck.scales[wl] + strip * p.ck.Lp + k, 16);
     }
-    kload -= span;
-    if (ACT8) {
-      q0.at += q0.leap;
-      q1.at += q1.leap;
-      q2.at += q2.leap;
-    } else {
-      xs.at += xs.leap;
-      rs.at += rs.leap;
-      gs.at += gs.leap;
-    }
-    ds.at += ds.leap;
     copies_commit();
   };
+  // the first rows are on their way before anything is waited for
+  if (wide) load(std::bool_constant<VEC>(), 0, k0), load(std::bool_constant<VEC>(), 1, k0 - span);
+  else load(std::false_type(), 0, k0), load(std::false_type(), 1, k0 - span);
 
-  long long left = n - k0;       // positions from this warp's first one to the end
-  load(0);
-  load(1);
+  const float2 rate = decay_rates(p.lam + e0, lane, cols), rate2 = __fmul2_rn(rate, two(LOG2E));
+  const float2 scale = near_scale(rate2);
+  const float2 nscale = make_float2(scale.x > 0.0f ? -1.0f / scale.x : 0.0f, scale.y > 0.0f ? -1.0f / scale.y : 0.0f);
+  const bool near = __all_sync(0xffffffffu, rate2.x >= NEAR_RATE2 && rate2.y >= NEAR_RATE2);
+  float2 carry = p.dh_last ? load_vec_pair(p.dh_last + (size_t)b * p.E + e0, lane, cols) : two(0.0f);
+  float2 dlam = two(0.0f);
   if (blocks > 1) cluster_sync();
-  for (int round = 0; round < rounds; ++round, left += span) {
-    const int buf = round & 1;
+
+  auto walk = [&](auto near_tag, auto wide_tag) {
+  constexpr bool NEAR = decltype(near_tag)::value, WIDE = decltype(wide_tag)::value;
+  int k = k0;                    // this warp's first position
+  for (int round = 0; round < rounds; ++round, k -= span) {
+    const int buf = round & 1, left = n - k;     // positions from this warp's first one to the end
     const Q* const in = rows0 + buf * 3 * ARRAY + half * LayQ::GROUP_STRIDE;
     const T* const dy = dy0 + buf * DY + half * Lay::GROUP_STRIDE;
-    const int mine = (int)min((long long)ROWS, left - half * ROWS);    // rows of this group (none: ≤ 0)
+    const int mine = min(ROWS, left - half * ROWS);    // rows of this group (none: ≤ 0)
     copies_wait<1>();
     __syncwarp();
-    uint2 scale[3];
+    uint2 factors[3];
     if (ACT8) {
 #pragma unroll
-      for (int i = 0; i < 3; ++i) scale[i] = *reinterpret_cast<const uint2*>(&sm.scales[buf][warp][i][half * ROWS]);
+      for (int i = 0; i < 3; ++i) factors[i] = *reinterpret_cast<const uint2*>(&sm.scales[buf][warp][i][half * ROWS]);
     }
     auto value = [&](int i, int j) {       // x, r or g of row j of this group
       const Q* const at = in + i * ARRAY + j * LayQ::CHANNELS;
       if constexpr (!ACT8) {
         return lane_pair(at, lane);
       } else {
-        const uint32_t word = j < 4 ? scale[i].x : scale[i].y;
+        const uint32_t word = j < 4 ? factors[i].x : factors[i].y;
         const float2 v = __fmul2_rn(act8::from_e4m3x2(reinterpret_cast<const uint16_t*>(at)[lane]),
                                     two(__uint_as_float((j % 4 ? word >> (8 * (j % 4)) : word) << 24 >> 1)));
         // what is read past the end is neither x = 0 nor a closed gate
@@ -162,17 +139,28 @@ __global__ void __launch_bounds__(WARPS * 32, (sizeof(T) == 2 ? 16 : 12) / WARPS
     // of each row: a, σ(g), and (s, β) for channels near 1, (σ(r), 1 − a²) otherwise
     float2 qa[ROWS], qg[ROWS], qs[ROWS], qb[ROWS];
     float2 a = two(1.0f), h = two(0.0f), D = two(0.0f);
-    auto first = [&](auto near_tag) {
+    if (left > 0) {
+      if (left < Lay::WARP_ROWS) {
+        // a position past the end has r = −∞, x = 0 and dy = 0
+        if constexpr (!ACT8) {
+          T* const to = (T*)rows0 + buf * 3 * ARRAY;
+          fill_rows<T, Lay>(to, wl, left, 0.0f);
+          fill_rows<T, Lay>(to + ARRAY, wl, left, -INFINITY);
+          fill_rows<T, Lay>(to + 2 * ARRAY, wl, left, 0.0f);
+        }
+        fill_rows<T, Lay>(dy0 + buf * DY, wl, left, 0.0f);
+        __syncwarp();
+      }
 #pragma unroll
       for (int j = 0; j < ROWS; ++j) {
         const float2 x = value(0, j), r = value(1, j), g = value(2, j);
         float2 beta;
-        if constexpr (decltype(near_tag)::value) {
+        if constexpr (NEAR) {
           const float2 d = sigmoid_den(r);
           qs[j] = make_float2(rsqrt_approx(d.x), rsqrt_approx(d.y));
           const float2 l2 = __fmul2_rn(__fmul2_rn(qs[j], qs[j]), rate2);
           qa[j] = near_decay(l2);
-          qb[j] = beta = __fmul2_rn(__fmul2_rn(qs[j], k), near_beta(l2));
+          qb[j] = beta = __fmul2_rn(__fmul2_rn(qs[j], scale), near_beta(l2));
           qg[j] = sigmoid2(g);
         } else {
           const Gates q = gates2(r, g, rate2);
@@ -187,10 +175,6 @@ __global__ void __launch_bounds__(WARPS * 32, (sizeof(T) == 2 ? 16 : 12) / WARPS
       }
 #pragma unroll
       for (int j = ROWS - 1; j >= 0; --j) D = __fmul2_rn(qa[j], __fadd2_rn(D, lane_pair(dy + j * Lay::CHANNELS, lane)));
-    };
-    if (left > 0) {
-      if (near) first(std::true_type());
-      else first(std::false_type());
     }
     const float2 oa = other_half(a), oh = other_half(h), oD = other_half(D);
     if (half == 0) {
@@ -220,22 +204,23 @@ __global__ void __launch_bounds__(WARPS * 32, (sizeof(T) == 2 ? 16 : 12) / WARPS
       }
       if (half) h = __ffma2_rn(oa, h, oh);
       else D = __ffma2_rn(oa, D, oD);
+      T* const dx = dx0 + (long long)(k + half * ROWS) * dx_step + 2 * lane;
+      T* const dr = dr0 + (long long)(k + half * ROWS) * dr_step + 2 * lane;
+      T* const dg = dg0 + (long long)(k + half * ROWS) * dg_step + 2 * lane;
       float2 G[ROWS];
 #pragma unroll
       for (int j = ROWS - 1; j >= 0; --j) {
         G[j] = __fadd2_rn(D, lane_pair(dy + j * Lay::CHANNELS, lane));
         D = __fmul2_rn(qa[j], G[j]);
       }
-      const bool all = wide && left >= Lay::WARP_ROWS;
-      auto second = [&](auto near_tag) {
 #pragma unroll
         for (int j = 0; j < ROWS; ++j) {
           const float2 x = value(0, j), sgx = __fmul2_rn(qg[j], x);
           float2 sr, beta, nv;      // nv = −σ(r) / β
-          if constexpr (decltype(near_tag)::value) {
+          if constexpr (NEAR) {
             sr = __fmul2_rn(qs[j], qs[j]);
             beta = qb[j];
-            nv = __fmul2_rn(qs[j], __fmul2_rn(nik, near_beta_inverse(__fmul2_rn(sr, rate2))));
+            nv = __fmul2_rn(qs[j], __fmul2_rn(nscale, near_beta_inverse(__fmul2_rn(sr, rate2))));
           } else {
             // 0 where the gate is closed (or u subnormal), as is the limit of all that it is part of
             const float2 rb = make_float2(qb[j].x < TINY ? 0.0f : rsqrt_approx(qb[j].x), qb[j].y < TINY ? 0.0f : rsqrt_approx(qb[j].y));
@@ -251,25 +236,21 @@ __global__ void __launch_bounds__(WARPS * 32, (sizeof(T) == 2 ? 16 : 12) / WARPS
           dlam = __fadd2_rn(dlam, dls);
           const float2 vdr = __fmul2_rn(__fmul2_rn(dls, rate), __ffma2_rn(sr, two(-1.0f), two(1.0f)));
           h = __ffma2_rn(qa[j], h, __fmul2_rn(beta, sgx));
-          if (all) {
-            store_whole_pair(dx + j * dx_step, vdx);
-            store_whole_pair(dr + j * dr_step, vdr);
-            store_whole_pair(dg + j * dg_step, vdg);
-          } else if (j < mine) {
-            store_pair<VEC>(dx + j * dx_step - 2 * lane, lane, cols, vdx);
-            store_pair<VEC>(dr + j * dr_step - 2 * lane, lane, cols, vdr);
-            store_pair<VEC>(dg + j * dg_step - 2 * lane, lane, cols, vdg);
-          }
-        }
-      };
-      if (near) second(std::true_type());
-      else second(std::false_type());
+          store_lane<WIDE>(row_at(dx, dx_step, j), j, mine, lane, cols, vdx);
+          store_lane<WIDE>(row_at(dr, dr_step, j), j, mine, lane, cols, vdr);
+          store_lane<WIDE>(row_at(dg, dg_step, j), j, mine, lane, cols, vdg);
+      }
     }
-    dx -= span * dx_step;
-    dr -= span * dr_step;
-    dg -= span * dg_step;
     __syncwarp();            // the warp has read its rows: their buffer takes the tile after the next
-    load(buf);
+    load(wide_tag, buf, k - 2 * span);
+  }
+  };
+  if (wide) {
+    if (near) walk(std::true_type(), std::bool_constant<VEC>());
+    else walk(std::false_type(), std::bool_constant<VEC>());
+  } else {
+    if (near) walk(std::true_type(), std::false_type());
+    else walk(std::false_type(), std::false_type());
   }
   if (p.dh0 && rank == 0 && warp == 0 && half == 0) store_pair<false>(p.dh0 + (size_t)b * p.E + e0, lane, cols, carry);
   for (long long i = n + (long long)(rank * WARPS + warp) * 2 + half; i < p.L; i += blocks * WARPS * 2) {   // rows past the end

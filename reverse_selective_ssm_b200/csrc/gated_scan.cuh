@@ -199,17 +199,6 @@ __device__ __forceinline__ void copies_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(PENDING) : "memory");
 }
 
-template <typename T>
-__device__ __forceinline__ uint32_t bits_twice(float v);
-template <>
-__device__ __forceinline__ uint32_t bits_twice<float>(float v) {
-  return __float_as_uint(v);
-}
-template <>
-__device__ __forceinline__ uint32_t bits_twice<bf16>(float v) {
-  return (__float_as_uint(v) >> 16) * 0x10001u;
-}
-
 // Threads of a warp and their rows.  LANES lanes hold a row of 2 · LANES
 // channels, two each, so a warp has 32 / LANES groups of ROWS consecutive rows;
 // in shared memory a group is followed by 64 bytes of nothing, which puts two
@@ -230,57 +219,41 @@ struct Layout {
   static __device__ __forceinline__ int chunk(int wl) { return at(wl / CHUNKS) + wl % CHUNKS * PER; }
 };
 
-// The rows of one warp on their way to shared memory.  A warp copies only the
-// rows that it reads itself, so a copy needs no barrier of the block, and its
-// address is a pointer that moves from tile to tile.
-template <typename T, bool VEC, typename LAY>
-struct RowStream {
-  const T* at;            // VEC: this lane's chunk of the next tile's first rows; else the warp's first row
-  long long step, leap;   // to the next row, and to the next tile
-  __device__ __forceinline__ void start(const void* base, long long row, long long ld, int dir, int e0, long long tile_rows,
-                                        int lane) {
-    step = dir * ld;
-    leap = tile_rows * step;
-    at = (const T*)base + row * ld + e0 + (VEC ? lane / LAY::CHUNKS * step + lane % LAY::CHUNKS * LAY::PER : 0);
-  }
-  // The next tile's rows into dst.
-  __device__ __forceinline__ void whole(T* dst, int lane) const {
-    dst += LAY::chunk(lane);
-#pragma unroll
-    for (int i = 0; i < LAY::WARP_ROWS; i += LAY::AT_ONCE) copy16(dst + LAY::at(i), at + i * step, 16);
-  }
-};
-
 __device__ __forceinline__ void copy_element(float* to, const float* from) {
   asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(to)), "l"(from) : "memory");
 }
 __device__ __forceinline__ void copy_element(bf16* to, const bf16* from) { *to = *from; }
 
-// The same where the tile has `rows` valid rows or `cols` channels only, or
-// where rows are not aligned: what lies past them is 0, and `fill` in rows past
-// the end (bf16 holds it).
-template <typename T, bool VEC, typename LAY>
-__device__ __noinline__ void copy_part(T* dst, const T* at, long long step, int lane, int rows, int cols, float fill) {
-  if (VEC) {
-    const int c = lane % LAY::CHUNKS * LAY::PER, bytes = min(max(cols - c, 0), LAY::PER) * (int)sizeof(T);
-    for (int i = 0; i < LAY::WARP_ROWS; i += LAY::AT_ONCE) {
-      T* const to = dst + LAY::chunk(lane) + LAY::at(i);
-      if (lane / LAY::CHUNKS + i < rows) {
-        copy16(to, bytes ? at + i * step : at - c, bytes);
-      } else {
-        const uint32_t f = bits_twice<T>(fill);
-        *reinterpret_cast<uint4*>(to) = make_uint4(f, f, f, f);
-      }
-    }
+// The rows of a warp from position k on, on their way to dst in shared memory.
+// A warp copies only the rows that it reads itself, so a copy needs no barrier
+// of the block.  `first` is position 0 of the sequence at the block's first
+// channel, `step` leads to the next position; both are the same for all the
+// block's threads.  Rows past the last position n − 1 take that one's values
+// (no test per copy; see fill_rows).  WIDE: rows start on 16-byte boundaries
+// and have all the block's channels; else channels from `cols` on are 0.
+template <typename T, bool WIDE, typename LAY>
+__device__ __forceinline__ void copy_rows(T* dst, const T* first, int step, int k, int n, int cols, int wl) {
+  if constexpr (WIDE) {
+    dst += LAY::chunk(wl);
+#pragma unroll
+    for (int i = 0; i < LAY::WARP_ROWS; i += LAY::AT_ONCE)
+      copy16(dst + LAY::at(i), first + (long long)min(k + i + wl / LAY::CHUNKS, n - 1) * step + wl % LAY::CHUNKS * LAY::PER, 16);
   } else {
-#pragma unroll 16
+#pragma unroll 8
     for (int i = 0; i < LAY::WARP_ROWS * LAY::CHANNELS; i += 32) {
-      const int row = (i + lane) / LAY::CHANNELS, c = (i + lane) % LAY::CHANNELS;
+      const int row = (i + wl) / LAY::CHANNELS, c = (i + wl) % LAY::CHANNELS;
       T* const to = dst + LAY::at(row) + c;
-      if (row < rows && c < cols) copy_element(to, at + row * step + c);
-      else *to = from_f32<T>(row < rows ? 0.0f : fill);
+      if (c < cols) copy_element(to, first + (long long)min(k + row, n - 1) * step + c);
+      else *to = from_f32<T>(0.0f);
     }
   }
+}
+// v in all channels of the rows from `rows` on, of a warp that has no more.
+template <typename T, typename LAY>
+__device__ __forceinline__ void fill_rows(T* dst, int wl, int rows, float v) {
+#pragma unroll 1
+  for (int row = rows; row < LAY::WARP_ROWS; ++row)
+    for (int c = wl; c < LAY::CHANNELS; c += 32) dst[LAY::at(row) + c] = from_f32<T>(v);
 }
 
 __device__ __forceinline__ float2 lane_pair(const float* row, int lane) {
@@ -291,9 +264,55 @@ __device__ __forceinline__ float2 lane_pair(const bf16* row, int lane) {
   return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
 }
 
+// Row j from p, a step of `step` elements (32 bits: one multiply-add forms the address).
+template <typename T>
+__device__ __forceinline__ T* row_at(T* p, int step, int j) {
+  return p + (long long)step * j;
+}
+
 __device__ __forceinline__ void store_whole_pair(float* at, float2 v) { *reinterpret_cast<float2*>(at) = v; }
 __device__ __forceinline__ void store_whole_pair(bf16* at, float2 v) {
   *reinterpret_cast<__nv_bfloat162*>(at) = __float22bfloat162_rn(v);
+}
+__device__ __forceinline__ void store_if(uint16_t* at, int j, int rows, uint16_t v) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.lt.s32 p, %0, %1;\n\t@p st.global.b16 [%2], %3;\n\t}" ::"r"(j), "r"(rows), "l"(at),
+               "h"(v)
+               : "memory");
+}
+// The larger magnitude of a lane's two channels, as the bits of a float (from 0x7f800000 on: not finite).
+__device__ __forceinline__ uint32_t lane_abs_max(const float* row, int lane) {
+  const float2 v = lane_pair(row, lane);
+  return max(__float_as_uint(v.x) & 0x7fffffffu, __float_as_uint(v.y) & 0x7fffffffu);
+}
+__device__ __forceinline__ uint32_t lane_abs_max(const bf16* row, int lane) {
+  const uint32_t w = reinterpret_cast<const uint32_t*>(row)[lane] & 0x7fff7fffu;
+  return max(w, w << 16) & 0xffff0000u;
+}
+
+// A lane's two channels at `at`, where j < rows (as a predicate, not a branch).
+// WIDE: both exist, on a boundary of two; else `cols` − 2·lane of them exist.
+template <bool WIDE>
+__device__ __forceinline__ void store_lane(float* at, int j, int rows, int lane, int cols, float2 v) {
+  if constexpr (WIDE) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.lt.s32 p, %0, %1;\n\t@p st.global.v2.f32 [%2], {%3, %4};\n\t}" ::"r"(j),
+                 "r"(rows), "l"(at), "f"(v.x), "f"(v.y)
+                 : "memory");
+  } else if (j < rows) {
+    if (2 * lane < cols) at[0] = v.x;
+    if (2 * lane + 1 < cols) at[1] = v.y;
+  }
+}
+template <bool WIDE>
+__device__ __forceinline__ void store_lane(bf16* at, int j, int rows, int lane, int cols, float2 v) {
+  const __nv_bfloat162 w = __float22bfloat162_rn(v);
+  if constexpr (WIDE) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.lt.s32 p, %0, %1;\n\t@p st.global.b32 [%2], %3;\n\t}" ::"r"(j), "r"(rows),
+                 "l"(at), "r"(*reinterpret_cast<const uint32_t*>(&w))
+                 : "memory");
+  } else if (j < rows) {
+    if (2 * lane < cols) at[0] = w.x;
+    if (2 * lane + 1 < cols) at[1] = w.y;
+  }
 }
 
 // Channels 2·lane and 2·lane + 1 of a row of `cols` channels.  VEC: the pair is aligned.
@@ -375,6 +394,12 @@ __device__ __forceinline__ float2 through_cluster(float4* box, float4 mine, int 
   return enters;
 }
 
+// A warp's arrival at named barrier `id` of it and the warp that waits there:
+// what it wrote before, the other reads after.  The barrier 0 of __syncthreads
+// is one of them, so the two kinds do not mix within a loop.
+__device__ __forceinline__ void pass_to(int id) { asm volatile("barrier.cta.arrive %0, 64;" ::"r"(id) : "memory"); }
+__device__ __forceinline__ void wait_at(int id) { asm volatile("barrier.cta.sync %0, 64;" ::"r"(id) : "memory"); }
+
 // The other half warp's value.
 __device__ __forceinline__ float2 other_half(float2 v) {
   return make_float2(__shfl_xor_sync(0xffffffffu, v.x, 16), __shfl_xor_sync(0xffffffffu, v.y, 16));
@@ -390,7 +415,7 @@ template <typename T, int LANES, int WARPS>
 struct FwdSmem {
   T in[2][3][WARPS * Layout<T, LANES, ROWS>::WARP_STRIDE];
   float4 maps[2][WARPS][LANES];
-  float2 carry[2][LANES];
+  float2 carry[WARPS][LANES];
 };
 template <typename T, int LANES, int WARPS>
 constexpr size_t fwd_smem_bytes(uint32_t blocks) {
@@ -399,7 +424,7 @@ constexpr size_t fwd_smem_bytes(uint32_t blocks) {
 
 // MODE 0: the recurrence; 1: also the states of a checkpoint; 2: and its 8 bits.
 template <typename T, bool VEC, int MODE, int LANES, int WARPS>
-__global__ void __launch_bounds__(WARPS * 32, (sizeof(T) == 2 ? (WARPS == 16 ? 32 : LANES == 16 ? 28 : 24) : 16) / WARPS)
+__global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
     gated_scan_kernel(const FwdArgs p, const uint32_t blocks) {
   typedef Layout<T, LANES, ROWS> Lay;
   typedef FwdSmem<T, LANES, WARPS> Smem;
@@ -419,68 +444,107 @@ __global__ void __launch_bounds__(WARPS * 32, (sizeof(T) == 2 ? (WARPS == 16 ? 3
   const int dir = p.forward ? 1 : -1;
   const int span = SPAN * (int)blocks;                 // positions of a round
   const int rounds = n > 0 ? (n - 1) / span + 1 : 0;
-  const int skip = (int)rank * SPAN + warp * Lay::WARP_ROWS;   // positions before this warp's in the first round
-  const long long row = (long long)b * p.L + (p.forward ? 0 : n - 1) + (long long)dir * skip;
-  const float2 rate2 = __fmul2_rn(decay_rates(p.lam + e0, lane, cols), two(LOG2E));
-  const float2 k = near_scale(rate2);
-  const bool near = __all_sync(0xffffffffu, rate2.x >= NEAR_RATE2 && rate2.y >= NEAR_RATE2);
-  float2 carry = p.h0 ? load_vec_pair(p.h0 + (size_t)b * p.E + e0, lane, cols) : two(0.0f);
+  const int k0 = (int)rank * SPAN + warp * Lay::WARP_ROWS;     // this warp's first position in the first round
+  const long long row0 = (long long)b * p.L + (p.forward ? 0 : n - 1);   // position 0
 
-  RowStream<T, VEC, Lay> xs, rs, gs;
-  xs.start(p.x, row, p.ldx, dir, e0, span, wl);
-  rs.start(p.r, row, p.ldr, dir, e0, span, wl);
-  gs.start(p.g, row, p.ldg, dir, e0, span, wl);
-  const long long out_step = dir * p.ldy, out_leap = span * out_step;
-  T* out = (T*)p.y + row * p.ldy + half * ROWS * out_step + e0 + 2 * lane;
-  const bool wide = VEC && cols == Lay::CHANNELS;
+  const T* const x0 = (const T*)p.x + row0 * p.ldx + e0;
+  const T* const r0 = (const T*)p.r + row0 * p.ldr + e0;
+  const T* const g0 = (const T*)p.g + row0 * p.ldg + e0;
+  T* const y0 = (T*)p.y + row0 * p.ldy + e0;
+  const int x_step = dir * (int)p.ldx, r_step = dir * (int)p.ldr, g_step = dir * (int)p.ldg, y_step = dir * (int)p.ldy;
   constexpr int ARRAY = WARPS * Lay::WARP_STRIDE;
   T* const rows0 = sm.in[0][0] + warp * Lay::WARP_STRIDE;
-  // A position past the end has r = −∞ and x = 0: a = 1, b = 0, and no other
-  // test is needed in the arithmetic.
-  auto load = [&](int buf, int rows) {
-    T* const to = rows0 + buf * 3 * ARRAY;
-    if (wide && rows >= Lay::WARP_ROWS) {
-      xs.whole(to, wl);
-      rs.whole(to + ARRAY, wl);
-      gs.whole(to + 2 * ARRAY, wl);
-    } else if (rows > 0) {
-      copy_part<T, VEC, Lay>(to, xs.at, xs.step, wl, rows, cols, 0.0f);
-      copy_part<T, VEC, Lay>(to + ARRAY, rs.at, rs.step, wl, rows, cols, -INFINITY);
-      copy_part<T, VEC, Lay>(to + 2 * ARRAY, gs.at, gs.step, wl, rows, cols, 0.0f);
+
+  const bool wide = VEC && cols == Lay::CHANNELS;
+  auto load = [&](auto wide_tag, int buf, int k) {
+    constexpr bool WIDE = decltype(wide_tag)::value;
+    if (k < n) {
+      T* const to = rows0 + buf * 3 * ARRAY;
+      copy_rows<T, WIDE, Lay>(to, x0, x_step, k, n, cols, wl);
+      copy_rows<T, WIDE, Lay>(to + ARRAY, r0, r_step, k, n, cols, wl);
+      copy_rows<T, WIDE, Lay>(to + 2 * ARRAY, g0, g_step, k, n, cols, wl);
     }
-    xs.at += xs.leap;
-    rs.at += rs.leap;
-    gs.at += gs.leap;
     copies_commit();
   };
+  // the first rows are on their way before anything is waited for
+  if (wide) load(std::bool_constant<VEC>(), 0, k0), load(std::bool_constant<VEC>(), 1, k0 + span);
+  else load(std::false_type(), 0, k0), load(std::false_type(), 1, k0 + span);
 
-  int left = n - skip;     // positions from this warp's first one to the end
-  load(0, left);
-  load(1, left - span);
+  const float2 rate2 = __fmul2_rn(decay_rates(p.lam + e0, lane, cols), two(LOG2E));
+  const float2 scale = near_scale(rate2);
+  const bool near = __all_sync(0xffffffffu, rate2.x >= NEAR_RATE2 && rate2.y >= NEAR_RATE2);
+  float2 carry = p.h0 ? load_vec_pair(p.h0 + (size_t)b * p.E + e0, lane, cols) : two(0.0f);
   if (blocks > 1) cluster_sync();   // every block of the cluster runs before its shared memory is written
-  for (int round = 0; round < rounds; ++round, left -= span) {
-    const int buf = round & 1;
+
+  auto scan = [&](auto near_tag, auto wide_tag) {
+  constexpr bool NEAR = decltype(near_tag)::value, WIDE = decltype(wide_tag)::value;
+  int k = k0;              // this warp's first position
+  for (int round = 0; round < rounds; ++round, k += span) {
+    const int buf = round & 1, left = n - k;      // positions from this warp's first one to the end
     const T* const in = rows0 + buf * 3 * ARRAY + half * Lay::GROUP_STRIDE;
     copies_wait<1>();
     __syncwarp();
     float2 P[ROWS], H[ROWS];     // row j's state is P[j] · (state that enters the group) + H[j]
     float2 a = two(1.0f), h = two(0.0f);
-    auto compute = [&](auto near_tag) {
+    if (left > 0) {
+      if (left < Lay::WARP_ROWS) {
+        // A position past the end has r = −∞ and x = 0: a = 1, b = 0, and no
+        // other test is needed in the arithmetic.
+        T* const to = rows0 + buf * 3 * ARRAY;
+        fill_rows<T, Lay>(to, wl, left, 0.0f);
+        fill_rows<T, Lay>(to + ARRAY, wl, left, -INFINITY);
+        fill_rows<T, Lay>(to + 2 * ARRAY, wl, left, 0.0f);
+        __syncwarp();
+      }
+      if constexpr (MODE == 2) {
+        // 8-bit copies: the channels that share a scale are one row of the
+        // warp.  Lane 8i + j gets the largest magnitude of row j of array i and
+        // works out that row's scale; the row's lanes have it by a shuffle.
+        const size_t at = ((size_t)b * strips + e0 / Lay::CHANNELS) * p.L + k;
+        uint32_t top = 0;
+#pragma unroll
+        for (int i = 0; i < 3; ++i)
+#pragma unroll
+          for (int j = 0; j < ROWS; ++j) {
+            const uint32_t m = __reduce_max_sync(0xffffffffu, lane_abs_max(in + i * ARRAY + j * Lay::CHANNELS, lane));
+            if (lane == i * ROWS + j) top = m;
+          }
+        const bool odd = __any_sync(0xffffffffu, top >= 0x7f800000u);
+        if (odd) {   // an infinity or a NaN does not count for the scale
+#pragma unroll 1
+          for (int c = 0; c < 3 * ROWS; ++c) {
+            const float2 v = lane_pair(in + c / ROWS * ARRAY + c % ROWS * Lay::CHANNELS, lane);
+            const uint32_t m = __reduce_max_sync(0xffffffffu, max(act8::finite_abs_bits(v.x), act8::finite_abs_bits(v.y)));
+            if (lane == c) top = m;
+          }
+        }
+        const uint32_t byte = act8::scale_byte(top);
+        const float down = act8::scale_down(byte);
+        if (lane < 3 * ROWS && lane % ROWS < left)
+          p.ck.scales[0][lane / ROWS * (p.ck.scales[1] - p.ck.scales[0]) + (size_t)(at / p.L) * p.ck.Lp + k + lane % ROWS] = (uint8_t)byte;
+#pragma unroll
+        for (int i = 0; i < 3; ++i) {
+          uint16_t* const q = reinterpret_cast<uint16_t*>(p.ck.q[i] + at * STRIP) + lane;
+#pragma unroll
+          for (int j = 0; j < ROWS; ++j) {
+            float2 v = lane_pair(in + i * ARRAY + j * Lay::CHANNELS, lane);
+            if (odd) v = make_float2(act8::nan_if_not_finite(v.x), act8::nan_if_not_finite(v.y));
+            v = __fmul2_rn(v, two(__shfl_sync(0xffffffffu, down, i * ROWS + j)));
+            store_if(q + j * (STRIP / 2), j, left, act8::to_e4m3x2(v.x, v.y));
+          }
+        }
+      }
 #pragma unroll
       for (int j = 0; j < ROWS; ++j) {
         float2 aj, bj;
-        coefficients<decltype(near_tag)::value>(lane_pair(in + j * Lay::CHANNELS, lane),
+        coefficients<NEAR>(lane_pair(in + j * Lay::CHANNELS, lane),
                                                 lane_pair(in + ARRAY + j * Lay::CHANNELS, lane),
-                                                lane_pair(in + 2 * ARRAY + j * Lay::CHANNELS, lane), rate2, k, aj, bj);
+                                                lane_pair(in + 2 * ARRAY + j * Lay::CHANNELS, lane), rate2, scale, aj, bj);
         a = j == 0 ? aj : __fmul2_rn(a, aj);
         h = j == 0 ? bj : __ffma2_rn(aj, h, bj);
         P[j] = a;
         H[j] = h;
       }
-    };
-    if (left > 0) {
-      if (near) compute(std::true_type());
-      else compute(std::false_type());
     }
     // the warp's map, and what its first half's does to the second half
     float4 map = make_float4(a.x, a.y, h.x, h.y), before = make_float4(1.0f, 1.0f, 0.0f, 0.0f);
@@ -490,60 +554,49 @@ __global__ void __launch_bounds__(WARPS * 32, (sizeof(T) == 2 ? (WARPS == 16 ? 3
       if (half) before = o;
       map = after(half ? map : o, half ? o : map);
     }
-    if (half == 0) sm.maps[buf][warp][lane] = map;
-    if (MODE == 2 && left > 0) {
-      // The channels that share a scale are one row of the warp.
-      const int k0 = n - left;
-      const size_t strip = (size_t)b * strips + e0 / Lay::CHANNELS;
-#pragma unroll
-      for (int i = 0; i < 3; ++i) {
-        uint16_t* const q = reinterpret_cast<uint16_t*>(p.ck.q[i] + (strip * p.L + k0) * STRIP) + lane;
-        uint32_t keep = 0;
-#pragma unroll
-        for (int j = 0; j < ROWS; ++j) {
-          const float2 v = lane_pair(in + i * ARRAY + j * STRIP, lane);
-          const uint32_t top = __reduce_max_sync(0xffffffffu, max(act8::finite_abs_bits(v.x), act8::finite_abs_bits(v.y)));
-          const uint32_t byte = act8::scale_byte(top);
-          const float down = act8::scale_down(byte);
-          if (lane == j) keep = byte;
-          if (j < left)
-            q[j * (STRIP / 2)] = act8::to_e4m3x2(act8::nan_if_not_finite(v.x) * down, act8::nan_if_not_finite(v.y) * down);
-        }
-        if (lane < ROWS && lane < left) p.ck.scales[i][strip * p.ck.Lp + k0 + lane] = (uint8_t)keep;
-      }
-    }
+    if (blocks > 1 && half == 0) sm.maps[buf][warp][lane] = map;
     __syncwarp();            // the warp has read its rows: their buffer takes the tile after the next
-    load(buf, left - 2 * span);
-    __syncthreads();
-    // the value that enters this tile, this warp, this group
-    float2 enters;
-    if (blocks > 1) {
+    load(wide_tag, buf, k + 2 * span);
+    float2 enters;           // the value that enters this warp
+    if (blocks == 1) {
+      // from warp to warp, and from the last one to the first one's next rows
+      if (round == 0 && warp == 0) {
+        enters = carry;
+      } else {
+        wait_at(warp);
+        enters = sm.carry[warp][lane];
+      }
+      carry = apply(map, enters);
+      if (round + 1 < rounds || warp + 1 < WARPS) {
+        const int next = (warp + 1) % WARPS;
+        if (half == 0) sm.carry[next][lane] = carry;
+        __syncwarp();
+        pass_to(next);
+      }
+    } else {
+      __syncthreads();
       float4 tile = sm.maps[buf][0][lane];
 #pragma unroll
       for (int w = 1; w < WARPS; ++w) tile = after(sm.maps[buf][w][lane], tile);
       enters = through_cluster<LANES>(box + buf * blocks * LANES, tile, warp * Lay::GROUPS + half, WARPS * Lay::GROUPS, lane,
                                       rank, blocks, carry);
-    } else {
-      enters = round == 0 ? carry : sm.carry[buf ^ 1][lane];
+      for (int w = 0; w < warp; ++w) enters = apply(sm.maps[buf][w][lane], enters);
     }
-    for (int w = 0; w < warp; ++w) enters = apply(sm.maps[buf][w][lane], enters);
-    if (blocks == 1 && warp == WARPS - 1) {
-      carry = apply(map, enters);
-      if (half == 0) sm.carry[buf][lane] = carry;
-    }
-    if (MODE >= 1 && warp % (TILE / Lay::WARP_ROWS) == 0 && half == 0 && left > 0)
-      reinterpret_cast<float2*>(p.ck.states + ((size_t)b * p.ck.tiles + (n - left) / TILE) * p.strips * STRIP + e0)[lane] = enters;
+    if (MODE >= 1 && k % TILE == 0 && half == 0 && left > 0)
+      reinterpret_cast<float2*>(p.ck.states + ((size_t)b * p.ck.tiles + k / TILE) * p.strips * STRIP + e0)[lane] = enters;
     if (Lay::GROUPS == 2) enters = apply(before, enters);
-    if (wide && left >= Lay::WARP_ROWS) {
+    T* const out = y0 + (long long)(k + half * ROWS) * y_step + 2 * lane;
 #pragma unroll
-      for (int j = 0; j < ROWS; ++j) store_whole_pair(out + j * out_step, __ffma2_rn(P[j], enters, H[j]));
-    } else {
-      const int mine = left - half * ROWS;
-#pragma unroll
-      for (int j = 0; j < ROWS; ++j)
-        if (j < mine) store_pair<VEC>(out + j * out_step - 2 * lane, lane, cols, __ffma2_rn(P[j], enters, H[j]));
-    }
-    out += out_leap;
+    for (int j = 0; j < ROWS; ++j)
+      store_lane<WIDE>(row_at(out, y_step, j), j, left - half * ROWS, lane, cols, __ffma2_rn(P[j], enters, H[j]));
+  }
+  };
+  if (wide) {
+    if (near) scan(std::true_type(), std::bool_constant<VEC>());
+    else scan(std::false_type(), std::bool_constant<VEC>());
+  } else {
+    if (near) scan(std::true_type(), std::false_type());
+    else scan(std::false_type(), std::false_type());
   }
   if (p.h_last && rank == 0 && warp == WARPS - 1 && half == 0)
     store_pair<false>(p.h_last + (size_t)b * p.E + e0, lane, cols, carry);
