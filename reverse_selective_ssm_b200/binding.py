@@ -7,6 +7,7 @@ shared library is missing or cannot be loaded, :func:`load` raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Dict, Optional, Sequence
@@ -439,42 +440,37 @@ def gated_dims(channels: int, dtype: torch.dtype, flags: int = 0) -> Dims:
     return Dims(channels, channels, 16, 1, 4, _CODES[dtype], flags)
 
 
-class _On:
-    """Where a call runs: its tensors' device is made the current one, its stream the one its own tensors are
-    allocated on (torch then reuses their memory in that stream's order).  ``stream``: None for the device's
-    current stream, a torch stream or a raw cudaStream_t."""
-
-    def __init__(self, device: torch.device, stream):
-        self.guards = []
-        if device.index != torch.cuda.current_device():
-            self.guards.append(torch.cuda.device(device))
-        if stream is not None:
+@contextlib.contextmanager
+def _elsewhere(device: torch.device, stream):
+    """The device of a call's tensors made the current one, and its stream the one that its own tensors are allocated
+    on (torch then reuses their memory in that stream's order); yields the raw stream."""
+    with torch.cuda.device(device):
+        if stream is None:
+            yield torch.cuda.current_stream(device).cuda_stream
+        else:
             if not hasattr(stream, "cuda_stream"):
                 stream = torch.cuda.ExternalStream(int(stream), device=device)
-            self.guards.append(torch.cuda.stream(stream))
-        self.device, self.stream = device, stream
+            with torch.cuda.stream(stream):
+                yield stream.cuda_stream
 
-    def __enter__(self) -> int:
-        for g in self.guards:
-            g.__enter__()
-        return (self.stream or torch.cuda.current_stream(self.device)).cuda_stream
 
-    def __exit__(self, *exc):
-        for g in reversed(self.guards):
-            g.__exit__(*exc)
+def _call_on(device: torch.device, stream, f):
+    """f(raw stream) on this device and stream (None: the device's current one; a torch stream or a raw
+    cudaStream_t).  Where the device is the current one and so is the stream, nothing is entered, and the raw stream is
+    asked for directly: contexts and stream objects cost more than the launch of a decoding step."""
+    if stream is None and device.index == torch.cuda.current_device():
+        return f(torch._C._cuda_getCurrentRawStream(device.index))
+    with _elsewhere(device, stream) as st:
+        return f(st)
 
 
 def _rows(t: torch.Tensor, M: int, E: int, dtype: torch.dtype, device: torch.device, name: str):
     """(pointer, row stride) of [M, E] rows whose elements are contiguous: a tensor or columns of a wider one."""
-    if t.shape != (M, E):
-        raise ValueError(f"{name} must be [{M}, {E}], got {tuple(t.shape)}")
-    if t.dtype != dtype:
-        raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.shape != (M, E) or t.dtype is not dtype or t.device != device:
+        raise ValueError(f"{name} must be {dtype} [{M}, {E}] on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
     row, col = t.stride()
-    if M == 1:
-        row = max(row, E)
+    if M == 1 and row < E:
+        row = E
     if (col != 1 and E > 1) or row < E:
         raise ValueError(f"{name}: rows must be contiguous and must not overlap (strides {(row, col)})")
     return t.data_ptr(), row
@@ -485,17 +481,26 @@ def _vec(t: Optional[torch.Tensor], shape, device: torch.device, name: str,
     """Pointer of a contiguous tensor of this shape and type (None: null)."""
     if t is None:
         return None
-    if t.shape != shape or t.dtype != dtype or t.device != device or not t.is_contiguous():
+    if t.shape != shape or t.dtype is not dtype or t.device != device or not t.is_contiguous():
         raise ValueError(f"{name} must be contiguous {dtype} {tuple(shape)} on {device}, got {t.dtype} "
                          f"{tuple(t.shape)} on {t.device}")
     return t.data_ptr()
 
 
+def _bytes(t: torch.Tensor, device: torch.device, name: str):
+    """(pointer, size in bytes) of a caller's buffer."""
+    if t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous and on {device}, got {t.device}")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
 def _gated_inputs(x, r, g, lam, h0, dims, B, L):
     if not x.is_cuda:
         raise ValueError("libr2l takes device tensors")
-    E, dtype, dev = dims.d_inner, _DTYPES[dims.dtype], x.device
-    (px, ldx), (pr, ldr), (pg, ldg) = (_rows(t, B * L, E, dtype, dev, n) for t, n in ((x, "x"), (r, "r"), (g, "g")))
+    M, E, dtype, dev = B * L, dims.d_inner, _DTYPES[dims.dtype], x.device
+    px, ldx = _rows(x, M, E, dtype, dev, "x")
+    pr, ldr = _rows(r, M, E, dtype, dev, "r")
+    pg, ldg = _rows(g, M, E, dtype, dev, "g")
     return GatedIn(px, pr, pg, ldx, ldr, ldg, _vec(lam, (E,), dev, "lam"), _vec(h0, (B, E), dev, "h0"))
 
 
@@ -503,21 +508,24 @@ def _gated_forward(x, r, g, lam, dims, B, L, h0, lengths, checkpoint, y, h_last,
     lib = load()
     gi = _gated_inputs(x, r, g, lam, h0, dims, B, L)
     E, dev = dims.d_inner, x.device
-    with _On(dev, stream) as st:
+
+    def call(st):
+        nonlocal y, h_last, checkpoint
         if y is None:
             y = torch.empty((B * L, E), dtype=x.dtype, device=dev)
         if h_last is None:
             h_last = torch.empty((B, E), dtype=torch.float32, device=dev)
         py, ldy = _rows(y, B * L, E, x.dtype, dev, "y")
-        args = [ctypes.byref(gi), py, ldy, _vec(h_last, (B, E), dev, "h_last"), ctypes.byref(dims), B, L,
-                _vec(lengths, (B,), dev, "lengths", torch.int32)]
-        if train:
-            if checkpoint is None:
-                checkpoint = torch.empty(lib.r2l_gated_scan_checkpoint_size(ctypes.byref(dims), B, L),
-                                         dtype=torch.uint8, device=dev)
-            args += [_ptr(checkpoint), checkpoint.numel() * checkpoint.element_size()]
-        args += [None if status is None else _ptr(status), st]
-        rc = (lib.r2l_gated_scan_train if train else lib.r2l_gated_scan)(*args)
+        ph = _vec(h_last, (B, E), dev, "h_last")
+        pl = _vec(lengths, (B,), dev, "lengths", torch.int32)
+        ps = None if status is None else _bytes(status, dev, "status")[0]
+        if not train:
+            return lib.r2l_gated_scan(gi, py, ldy, ph, dims, B, L, pl, ps, st)
+        if checkpoint is None:
+            checkpoint = torch.empty(lib.r2l_gated_scan_checkpoint_size(dims, B, L), dtype=torch.uint8, device=dev)
+        return lib.r2l_gated_scan_train(gi, py, ldy, ph, dims, B, L, pl, *_bytes(checkpoint, dev, "checkpoint"), ps, st)
+
+    rc = _call_on(dev, stream, call)
     if check and rc != 0:
         raise R2LError(rc, "r2l_gated_scan_train" if train else "r2l_gated_scan")
     return y, h_last, checkpoint
@@ -581,20 +589,25 @@ def gated_scan_backward(dy: torch.Tensor, lam: torch.Tensor, dims: Dims, B: int,
         if x is None or r is None or g is None:
             raise ValueError("x, r and g are needed unless the checkpoint holds them (R2L_FLAG_ACT8)")
         gi = _gated_inputs(x, r, g, lam, None, dims, B, L)
-    with _On(dev, stream) as st:
-        dx, dr, dg = (torch.empty((M, E), dtype=dtype, device=dev) if t is None else t for t in (dx, dr, dg))
-        out = {"dx": dx, "dr": dr, "dg": dg, "dlam": torch.empty(E, dtype=torch.float32, device=dev),
-               "dh0": torch.empty((B, E), dtype=torch.float32, device=dev)}
-        if workspace is None:
-            workspace = torch.empty(gated_scan_backward_workspace_size(dims, B, L), dtype=torch.uint8, device=dev)
+    out = {"dx": dx, "dr": dr, "dg": dg}
+
+    def call(st):
+        ws = workspace
+        if ws is None:
+            ws = torch.empty(gated_scan_backward_workspace_size(dims, B, L), dtype=torch.uint8, device=dev)
+        for n, t in out.items():
+            if t is None:
+                out[n] = torch.empty((M, E), dtype=dtype, device=dev)
+        out["dlam"] = torch.empty(E, dtype=torch.float32, device=dev)
+        out["dh0"] = torch.empty((B, E), dtype=torch.float32, device=dev)
         (pdx, ldx), (pdr, ldr), (pdg, ldg) = (_rows(out[n], M, E, dtype, dev, n) for n in ("dx", "dr", "dg"))
         gr = GatedGrads(pdx, pdr, pdg, ldx, ldr, ldg, out["dlam"].data_ptr(), out["dh0"].data_ptr())
         pdy, ld_dy = _rows(dy, M, E, dtype, dev, "dy")
-        rc = lib.r2l_gated_scan_backward(ctypes.byref(gi), pdy, ld_dy, _vec(dh_last, (B, E), dev, "dh_last"),
-                                         ctypes.byref(gr), ctypes.byref(dims), B, L,
-                                         _vec(lengths, (B,), dev, "lengths", torch.int32), _ptr(checkpoint),
-                                         checkpoint.numel() * checkpoint.element_size(), _ptr(workspace),
-                                         workspace.numel() * workspace.element_size(), st)
+        return lib.r2l_gated_scan_backward(gi, pdy, ld_dy, _vec(dh_last, (B, E), dev, "dh_last"), gr, dims, B, L,
+                                           _vec(lengths, (B,), dev, "lengths", torch.int32),
+                                           *_bytes(checkpoint, dev, "checkpoint"), *_bytes(ws, dev, "workspace"), st)
+
+    rc = _call_on(dev, stream, call)
     if check and rc != 0:
         raise R2LError(rc, "r2l_gated_scan_backward")
     return out
@@ -615,14 +628,18 @@ def act8_pack(x: torch.Tensor, B: int, L: int, lengths: Optional[torch.Tensor] =
     M, cols, dev = B * L, x.shape[1], x.device
     groups = -(-cols // ACT8_GROUP)
     px, ldx = _rows(x, M, cols, x.dtype, dev, "x")
-    with _On(dev, stream) as st:
+
+    def call(st):
+        nonlocal q, scales
         if q is None:
             q = torch.empty((M, cols), dtype=torch.float8_e4m3fn, device=dev)
         if scales is None:
             scales = torch.empty((M, groups), dtype=torch.uint8, device=dev)
         pq, ldq = _rows(q, M, cols, torch.float8_e4m3fn, dev, "q")
-        rc = lib.r2l_act8_pack(px, ldx, _CODES[x.dtype], B, L, cols, _vec(lengths, (B,), dev, "lengths", torch.int32),
-                               pq, ldq, _vec(scales, (M, groups), dev, "scales", torch.uint8), st)
+        return lib.r2l_act8_pack(px, ldx, _CODES[x.dtype], B, L, cols, _vec(lengths, (B,), dev, "lengths", torch.int32),
+                                 pq, ldq, _vec(scales, (M, groups), dev, "scales", torch.uint8), st)
+
+    rc = _call_on(dev, stream, call)
     if check and rc != 0:
         raise R2LError(rc, "r2l_act8_pack")
     return q, scales
@@ -644,13 +661,17 @@ def act8_unpack(q: torch.Tensor, scales: torch.Tensor, B: int, L: int, dtype: to
     if dtype not in _CODES:
         raise ValueError("the output is bf16 or fp32")
     pq, ldq = _rows(q, M, cols, torch.float8_e4m3fn, dev, "q")
-    with _On(dev, stream) as st:
+
+    def call(st):
+        nonlocal out
         if out is None:
             out = torch.empty((M, cols), dtype=dtype, device=dev)
         po, ldo = _rows(out, M, cols, dtype, dev, "out")
-        rc = lib.r2l_act8_unpack(pq, ldq, _vec(scales, (M, -(-cols // ACT8_GROUP)), dev, "scales", torch.uint8),
-                                 _CODES[dtype], B, L, cols, _vec(lengths, (B,), dev, "lengths", torch.int32), po, ldo,
-                                 st)
+        return lib.r2l_act8_unpack(pq, ldq, _vec(scales, (M, -(-cols // ACT8_GROUP)), dev, "scales", torch.uint8),
+                                   _CODES[dtype], B, L, cols, _vec(lengths, (B,), dev, "lengths", torch.int32), po, ldo,
+                                   st)
+
+    rc = _call_on(dev, stream, call)
     if check and rc != 0:
         raise R2LError(rc, "r2l_act8_unpack")
     return out

@@ -64,6 +64,7 @@ __global__ void __launch_bounds__(WARPS * 32, (sizeof(T) == 2 || WARPS == 8 ? 16
   const int k0 = (rounds - 1) * span + (int)(blocks - 1 - rank) * SPAN + warp * Lay::WARP_ROWS;
   const long long row0 = (long long)b * p.L + (p.forward ? 0 : n - 1);   // position 0
   const size_t strip = (size_t)b * p.strips + e0 / STRIP;
+  const bool wide = VEC && cols == Lay::CHANNELS;
   const Q* in0[3];          // x, r, g: position 0
   int in_step[3];
   if constexpr (ACT8) {     // rows of 64 bytes in scan order
@@ -84,16 +85,21 @@ __global__ void __launch_bounds__(WARPS * 32, (sizeof(T) == 2 || WARPS == 8 ? 16
   Q* const rows0 = sm.in[0][0] + warp * LayQ::WARP_STRIDE;
   T* const dy0 = sm.dy[0] + warp * Lay::WARP_STRIDE;
 
-  const bool wide = VEC && cols == Lay::CHANNELS;
   auto load = [&](auto wide_tag, int buf, int k) {
     constexpr bool WIDE = decltype(wide_tag)::value;
     if (k >= 0 && k < n) {
-      Q* const to = rows0 + buf * 3 * ARRAY;
 #pragma unroll
-      for (int i = 0; i < 3; ++i) copy_rows<Q, WIDE || ACT8, LayQ>(to + i * ARRAY, in0[i], in_step[i], k, n, cols, wl);
-      copy_rows<T, WIDE, Lay>(dy0 + buf * DY, first_dy, dy_step, k, n, cols, wl);
-      if (wl < BL / 2) copy16(sm.states[buf][warp] + 4 * wl, states0 + (long long)(k / TILE) * (p.strips * STRIP) + 4 * wl, 16);
-      if (ACT8 && wl < 3) copy16(sm.scales[buf][warp][wl], p.ck.scales[wl] + strip * p.ck.Lp + k, 16);
+      for (int i = 0; i < 3; ++i) {
+        if constexpr (WIDE || ACT8)
+          copy_rows<Q, LayQ>(smem_addr(rows0 + (buf * 3 + i) * ARRAY + LayQ::chunk(wl)), in0[i] + LayQ::channel(wl), in_step[i], k, n, wl);
+        else
+          copy_elements<Q, LayQ>(rows0 + (buf * 3 + i) * ARRAY, in0[i], in_step[i], k, n, cols, wl);
+      }
+      if constexpr (WIDE) copy_rows<T, Lay>(smem_addr(dy0 + buf * DY + Lay::chunk(wl)), first_dy + Lay::channel(wl), dy_step, k, n, wl);
+      else copy_elements<T, Lay>(dy0 + buf * DY, first_dy, dy_step, k, n, cols, wl);
+      if (wl < BL / 2)
+        copy16(smem_addr(sm.states[buf][warp] + 4 * wl), states0 + (long long)(k / TILE) * (p.strips * STRIP) + 4 * wl);
+      if (ACT8 && wl < 3) copy16(smem_addr(sm.scales[buf][warp][wl]), p.ck.scales[wl] + strip * p.ck.Lp + k);
     }
     copies_commit();
   };

@@ -189,9 +189,9 @@ __device__ __forceinline__ void write_status(const int32_t* lengths, int B, int 
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
-// 16 bytes to shared memory, the first `bytes` of them from src (the rest are zeros).
-__device__ __forceinline__ void copy16(void* dst, const void* src, int bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_addr(dst)), "l"(src), "r"(bytes) : "memory");
+// 16 bytes to an address of shared memory.
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int PENDING>
@@ -216,7 +216,8 @@ struct Layout {
   static_assert(ROWS % AT_ONCE == 0 || AT_ONCE == WARP_ROWS, "at(i + j) = at(i) + at(j) for the rows of a copy");
   static __device__ __forceinline__ int at(int row) { return row / ROWS * GROUP_STRIDE + row % ROWS * CHANNELS; }
   // This lane's chunk of the first rows that are copied at once.
-  static __device__ __forceinline__ int chunk(int wl) { return at(wl / CHUNKS) + wl % CHUNKS * PER; }
+  static __device__ __forceinline__ int chunk(int wl) { return at(wl / CHUNKS) + channel(wl); }
+  static __device__ __forceinline__ int channel(int wl) { return wl % CHUNKS * PER; }
 };
 
 __device__ __forceinline__ void copy_element(float* to, const float* from) {
@@ -226,26 +227,28 @@ __device__ __forceinline__ void copy_element(bf16* to, const bf16* from) { *to =
 
 // The rows of a warp from position k on, on their way to dst in shared memory.
 // A warp copies only the rows that it reads itself, so a copy needs no barrier
-// of the block.  `first` is position 0 of the sequence at the block's first
-// channel, `step` leads to the next position; both are the same for all the
-// block's threads.  Rows past the last position n − 1 take that one's values
-// (no test per copy; see fill_rows).  WIDE: rows start on 16-byte boundaries
-// and have all the block's channels; else channels from `cols` on are 0.
-template <typename T, bool WIDE, typename LAY>
-__device__ __forceinline__ void copy_rows(T* dst, const T* first, int step, int k, int n, int cols, int wl) {
-  if constexpr (WIDE) {
-    dst += LAY::chunk(wl);
+// of the block.  `step` leads to the next position.  Rows past the last
+// position n − 1 take that one's values (no test per copy; see fill_rows).
+// copy_rows: rows start on 16-byte boundaries and have all the block's
+// channels; `first` is position 0 at this lane's channel(), `dst` this
+// lane's chunk of the warp's rows: an address is one multiply-add.
+template <typename T, typename LAY>
+__device__ __forceinline__ void copy_rows(uint32_t dst, const T* first, int step, int k, int n, int wl) {
+  k += wl / LAY::CHUNKS;
 #pragma unroll
-    for (int i = 0; i < LAY::WARP_ROWS; i += LAY::AT_ONCE)
-      copy16(dst + LAY::at(i), first + (long long)min(k + i + wl / LAY::CHUNKS, n - 1) * step + wl % LAY::CHUNKS * LAY::PER, 16);
-  } else {
+  for (int i = 0; i < LAY::WARP_ROWS; i += LAY::AT_ONCE)
+    copy16(dst + LAY::at(i) * (int)sizeof(T), first + (long long)min(k + i, n - 1) * step);
+}
+// copy_elements: any rows, of which `cols` channels exist (the others are 0);
+// `first` is position 0 at the block's first channel.
+template <typename T, typename LAY>
+__device__ __forceinline__ void copy_elements(T* dst, const T* first, int step, int k, int n, int cols, int wl) {
 #pragma unroll 8
-    for (int i = 0; i < LAY::WARP_ROWS * LAY::CHANNELS; i += 32) {
-      const int row = (i + wl) / LAY::CHANNELS, c = (i + wl) % LAY::CHANNELS;
-      T* const to = dst + LAY::at(row) + c;
-      if (c < cols) copy_element(to, first + (long long)min(k + row, n - 1) * step + c);
-      else *to = from_f32<T>(0.0f);
-    }
+  for (int i = 0; i < LAY::WARP_ROWS * LAY::CHANNELS; i += 32) {
+    const int row = (i + wl) / LAY::CHANNELS, c = (i + wl) % LAY::CHANNELS;
+    T* const to = dst + LAY::at(row) + c;
+    if (c < cols) copy_element(to, first + (long long)min(k + row, n - 1) * step + c);
+    else *to = from_f32<T>(0.0f);
   }
 }
 // v in all channels of the rows from `rows` on, of a warp that has no more.
@@ -447,22 +450,30 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
   const int k0 = (int)rank * SPAN + warp * Lay::WARP_ROWS;     // this warp's first position in the first round
   const long long row0 = (long long)b * p.L + (p.forward ? 0 : n - 1);   // position 0
 
-  const T* const x0 = (const T*)p.x + row0 * p.ldx + e0;
-  const T* const r0 = (const T*)p.r + row0 * p.ldr + e0;
-  const T* const g0 = (const T*)p.g + row0 * p.ldg + e0;
+  const bool wide = VEC && cols == Lay::CHANNELS;
+  const int c0 = e0 + (wide ? Lay::channel(wl) : 0);
+  const T* const x0 = (const T*)p.x + row0 * p.ldx + c0;
+  const T* const r0 = (const T*)p.r + row0 * p.ldr + c0;
+  const T* const g0 = (const T*)p.g + row0 * p.ldg + c0;
   T* const y0 = (T*)p.y + row0 * p.ldy + e0;
   const int x_step = dir * (int)p.ldx, r_step = dir * (int)p.ldr, g_step = dir * (int)p.ldg, y_step = dir * (int)p.ldy;
   constexpr int ARRAY = WARPS * Lay::WARP_STRIDE;
   T* const rows0 = sm.in[0][0] + warp * Lay::WARP_STRIDE;
 
-  const bool wide = VEC && cols == Lay::CHANNELS;
+  const uint32_t chunk0 = smem_addr(rows0 + Lay::chunk(wl));
   auto load = [&](auto wide_tag, int buf, int k) {
-    constexpr bool WIDE = decltype(wide_tag)::value;
     if (k < n) {
-      T* const to = rows0 + buf * 3 * ARRAY;
-      copy_rows<T, WIDE, Lay>(to, x0, x_step, k, n, cols, wl);
-      copy_rows<T, WIDE, Lay>(to + ARRAY, r0, r_step, k, n, cols, wl);
-      copy_rows<T, WIDE, Lay>(to + 2 * ARRAY, g0, g_step, k, n, cols, wl);
+      if constexpr (decltype(wide_tag)::value) {
+        const uint32_t to = chunk0 + buf * (3 * ARRAY * (int)sizeof(T));
+        copy_rows<T, Lay>(to, x0, x_step, k, n, wl);
+        copy_rows<T, Lay>(to + ARRAY * (int)sizeof(T), r0, r_step, k, n, wl);
+        copy_rows<T, Lay>(to + 2 * ARRAY * (int)sizeof(T), g0, g_step, k, n, wl);
+      } else {
+        T* const to = rows0 + buf * 3 * ARRAY;
+        copy_elements<T, Lay>(to, x0, x_step, k, n, cols, wl);
+        copy_elements<T, Lay>(to + ARRAY, r0, r_step, k, n, cols, wl);
+        copy_elements<T, Lay>(to + 2 * ARRAY, g0, g_step, k, n, cols, wl);
+      }
     }
     copies_commit();
   };
