@@ -395,7 +395,8 @@ R2L_API r2l_status r2l_sidecar_forward_train(const void *hidden, void *out, cons
  * of rows all start on 16-byte boundaries with strides that are multiples of
  * 16 bytes runs faster.  No output may overlap an input, except h_last = h0
  * and dh0 = dh_last.  lengths as for r2l_sidecar_forward (clamped to [0, L];
- * a sequence of length 0 passes its state through).
+ * a sequence of length 0 passes its state through).  E and L up to 2^30 and
+ * B · L · E up to 2^50; more returns R2L_ERR_UNSUPPORTED.
  * ------------------------------------------------------------------------- */
 #define R2L_GATED_RATE 8.0f
 #define R2L_GATED_TILE 64   /* positions between two states of a checkpoint */
@@ -455,7 +456,8 @@ R2L_API size_t r2l_gated_scan_backward_workspace_size(const r2l_dims *dims, int 
  * in: x, r, g and lam as given to the forward (h0 is not read: the checkpoint
  * has it).  With R2L_FLAG_ACT8 x, r and g are not read either and may be NULL;
  * the gradient is then the formula at the values that the checkpoint's 8 bits
- * stand for, each tile's states recomputed from its exact first one.
+ * stand for, each tile's states recomputed from its exact first one.  Gates at
+ * ±∞ are kept as ±256 there, which closes and opens them just the same.
  * dims, B, L and lengths as given to r2l_gated_scan_train; dims->flags too.
  * Every sum runs in a fixed order: results are bitwise reproducible.
  * workspace ≥ r2l_gated_scan_backward_workspace_size(dims, B, L) bytes,

@@ -26,9 +26,12 @@ r2l_status run_backward(const BwdArgs& p, Split c, cudaStream_t st) {
   return launch(gated_bwd_kernel<T, VEC, ACT8, 8>, p, jobs, c.blocks, 256, bwd_smem_bytes<T, ACT8, 8>(c.blocks), st);
 }
 
-// Shares of dlam, one row for each block of channels' blocks.
+// Rows of the shares of dlam, and of their sums where one launch does not add them all.
+long long part_rows(const r2l_dims* d, int B, int L) { return (long long)B * backward_split(d, B, L).blocks; }
+long long sum_rows(long long rows) { return rows > DLAM_ROWS ? (rows - 1) / DLAM_ROWS + 1 : 0; }
 size_t part_bytes(const r2l_dims* d, int B, int L) {
-  return (size_t)B * backward_split(d, B, L).blocks * align_up(d->d_inner, STRIP) * sizeof(float);
+  const long long rows = part_rows(d, B, L);
+  return (size_t)(rows + sum_rows(rows)) * align_up(d->d_inner, STRIP) * sizeof(float);
 }
 
 }  // namespace
@@ -36,7 +39,8 @@ size_t part_bytes(const r2l_dims* d, int B, int L) {
 extern "C" {
 
 size_t r2l_gated_scan_backward_workspace_size(const r2l_dims* dims, int B, int L) {
-  return valid_dims(dims, B, L) && fits(B, L, dims->d_inner) ? kAlign + align_up(part_bytes(dims, B, L), kAlign) : 0;
+  return valid_dims(dims, B, L) && fits(B, L, dims->d_inner) && sum_rows(part_rows(dims, B, L)) <= 65535
+             ? kAlign + align_up(part_bytes(dims, B, L), kAlign) : 0;
 }
 
 r2l_status r2l_gated_scan_backward(const r2l_gated_in* in, const void* dy, int ld_dy, const float* dh_last,
@@ -68,7 +72,7 @@ r2l_status r2l_gated_scan_backward(const r2l_gated_in* in, const void* dy, int l
   if (!aligned(in->lam, 4) || !aligned(dh_last, 4) || !aligned(grads->dlam, 4) || !aligned(grads->dh0, 4) ||
       !aligned(lengths, 4))
     return R2L_ERR_ALIGNMENT;
-  if (!fits(B, L, E)) return R2L_ERR_UNSUPPORTED;
+  if (!fits(B, L, E) || sum_rows(part_rows(dims, B, L)) > 65535) return R2L_ERR_UNSUPPORTED;
   const CkptPlan k = plan_checkpoint(dims, B, L);
   if (!checkpoint || checkpoint_bytes < k.total) return R2L_ERR_WORKSPACE;
   if (!workspace || workspace_bytes < r2l_gated_scan_backward_workspace_size(dims, B, L)) return R2L_ERR_WORKSPACE;
@@ -96,7 +100,16 @@ r2l_status r2l_gated_scan_backward(const r2l_gated_in* in, const void* dy, int l
     if (act8) R2L_TRY((vec ? run_backward<float, true, true> : run_backward<float, false, true>)(p, c, st));
     else R2L_TRY((vec ? run_backward<float, true, false> : run_backward<float, false, false>)(p, c, st));
   }
-  gated_dlam_kernel<<<(E + 31) / 32, 256, 0, st>>>(p.part, (int)(B * c.blocks), p.strips * STRIP, p.lam, E, grads->dlam);
+  const int width = p.strips * STRIP, rows = (int)part_rows(dims, B, L), sums = (int)sum_rows(rows);
+  const dim3 by_channels((E + 31) / 32);
+  if (sums) {
+    float* const more = p.part + (size_t)rows * width;
+    gated_dlam_kernel<<<dim3(by_channels.x, sums), 256, 0, st>>>(p.part, rows, DLAM_ROWS, width, nullptr, E, more);
+    R2L_LAUNCH_CHECK();
+    gated_dlam_kernel<<<by_channels, 256, 0, st>>>(more, sums, sums, width, p.lam, E, grads->dlam);
+  } else {
+    gated_dlam_kernel<<<by_channels, 256, 0, st>>>(p.part, rows, rows, width, p.lam, E, grads->dlam);
+  }
   R2L_LAUNCH_CHECK();
   return R2L_OK;
 }

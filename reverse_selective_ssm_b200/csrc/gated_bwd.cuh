@@ -116,140 +116,140 @@ __global__ void __launch_bounds__(WARPS * 32, (sizeof(T) == 2 || WARPS == 8 ? 16
   if (blocks > 1) cluster_sync();
 
   auto walk = [&](auto near_tag, auto wide_tag) {
-  constexpr bool NEAR = decltype(near_tag)::value, WIDE = decltype(wide_tag)::value;
-  int k = k0;                    // this warp's first position
-  for (int round = 0; round < rounds; ++round, k -= span) {
-    const int buf = round & 1, left = n - k;     // positions from this warp's first one to the end
-    const Q* const in = rows0 + buf * 3 * ARRAY + half * LayQ::GROUP_STRIDE;
-    const T* const dy = dy0 + buf * DY + half * Lay::GROUP_STRIDE;
-    const int mine = min(ROWS, left - half * ROWS);    // rows of this group (none: ≤ 0)
-    copies_wait<1>();
-    __syncwarp();
-    uint2 factors[3];
-    if (ACT8) {
+    constexpr bool NEAR = decltype(near_tag)::value, WIDE = decltype(wide_tag)::value;
+    int k = k0;                    // this warp's first position
+    for (int round = 0; round < rounds; ++round, k -= span) {
+      const int buf = round & 1, left = n - k;     // positions from this warp's first one to the end
+      const Q* const in = rows0 + buf * 3 * ARRAY + half * LayQ::GROUP_STRIDE;
+      const T* const dy = dy0 + buf * DY + half * Lay::GROUP_STRIDE;
+      const int mine = min(ROWS, left - half * ROWS);    // rows of this group (none: ≤ 0)
+      copies_wait<1>();
+      __syncwarp();
+      uint2 factors[3];
+      if (ACT8) {
 #pragma unroll
-      for (int i = 0; i < 3; ++i) factors[i] = *reinterpret_cast<const uint2*>(&sm.scales[buf][warp][i][half * ROWS]);
-    }
-    auto value = [&](int i, int j) {       // x, r or g of row j of this group
-      const Q* const at = in + i * ARRAY + j * LayQ::CHANNELS;
-      if constexpr (!ACT8) {
-        return lane_pair(at, lane);
-      } else {
-        const uint32_t word = j < 4 ? factors[i].x : factors[i].y;
-        const float2 v = __fmul2_rn(act8::from_e4m3x2(reinterpret_cast<const uint16_t*>(at)[lane]),
-                                    two(__uint_as_float((j % 4 ? word >> (8 * (j % 4)) : word) << 24 >> 1)));
-        // what is read past the end is neither x = 0 nor a closed gate
-        return mine == ROWS ? v : j < mine ? v : two(i == 1 ? -INFINITY : 0.0f);
+        for (int i = 0; i < 3; ++i) factors[i] = *reinterpret_cast<const uint2*>(&sm.scales[buf][warp][i][half * ROWS]);
       }
-    };
-    // of each row: a, σ(g), and (s, β) for channels near 1, (σ(r), 1 − a²) otherwise
-    float2 qa[ROWS], qg[ROWS], qs[ROWS], qb[ROWS];
-    float2 a = two(1.0f), h = two(0.0f), D = two(0.0f);
-    if (left > 0) {
-      if (left < Lay::WARP_ROWS) {
-        // a position past the end has r = −∞, x = 0 and dy = 0
+      auto value = [&](int i, int j) {       // x, r or g of row j of this group
+        const Q* const at = in + i * ARRAY + j * LayQ::CHANNELS;
         if constexpr (!ACT8) {
-          T* const to = (T*)rows0 + buf * 3 * ARRAY;
-          fill_rows<T, Lay>(to, wl, left, 0.0f);
-          fill_rows<T, Lay>(to + ARRAY, wl, left, -INFINITY);
-          fill_rows<T, Lay>(to + 2 * ARRAY, wl, left, 0.0f);
-        }
-        fill_rows<T, Lay>(dy0 + buf * DY, wl, left, 0.0f);
-        __syncwarp();
-      }
-#pragma unroll
-      for (int j = 0; j < ROWS; ++j) {
-        const float2 x = value(0, j), r = value(1, j), g = value(2, j);
-        float2 beta;
-        if constexpr (NEAR) {
-          const float2 d = sigmoid_den(r);
-          qs[j] = make_float2(rsqrt_approx(d.x), rsqrt_approx(d.y));
-          const float2 l2 = __fmul2_rn(__fmul2_rn(qs[j], qs[j]), rate2);
-          qa[j] = near_decay(l2);
-          qb[j] = beta = __fmul2_rn(__fmul2_rn(qs[j], scale), near_beta(l2));
-          qg[j] = sigmoid2(g);
+          return lane_pair(at, lane);
         } else {
-          const Gates q = gates2(r, g, rate2);
-          qa[j] = q.a;
-          qg[j] = q.sg;
-          qs[j] = q.sr;
-          qb[j] = q.u;
-          beta = make_float2(sqrt_approx(q.u.x), sqrt_approx(q.u.y));
+          const uint32_t word = j < 4 ? factors[i].x : factors[i].y;
+          const float2 v = __fmul2_rn(act8::from_e4m3x2(reinterpret_cast<const uint16_t*>(at)[lane]),
+                                      two(__uint_as_float((j % 4 ? word >> (8 * (j % 4)) : word) << 24 >> 1)));
+          // what is read past the end is neither x = 0 nor a closed gate
+          return mine == ROWS ? v : j < mine ? v : two(i == 1 ? -INFINITY : 0.0f);
         }
-        h = __ffma2_rn(qa[j], h, __fmul2_rn(beta, __fmul2_rn(qg[j], x)));
-        a = j == 0 ? qa[j] : __fmul2_rn(a, qa[j]);
-      }
-#pragma unroll
-      for (int j = ROWS - 1; j >= 0; --j) D = __fmul2_rn(qa[j], __fadd2_rn(D, lane_pair(dy + j * Lay::CHANNELS, lane)));
-    }
-    const float2 oa = other_half(a), oh = other_half(h), oD = other_half(D);
-    if (half == 0) {
-      const float4 map = after(make_float4(a.x, a.y, D.x, D.y), make_float4(oa.x, oa.y, oD.x, oD.y));
-      sm.maps[buf][warp][lane] = map;
-      sm.h[buf][warp][lane] = __ffma2_rn(oa, h, oh);
-    }
-    __syncthreads();
-    if (blocks > 1) {
-      float4 tile = sm.maps[buf][WARPS - 1][lane];
-#pragma unroll
-      for (int w = WARPS - 2; w >= 0; --w) tile = after(sm.maps[buf][w][lane], tile);
-      D = through_cluster<BL>(box + buf * blocks * BL, tile, warp * 2 + half, WARPS * 2, lane, rank, blocks, carry);
-    } else {
-      D = round == 0 ? carry : sm.carry[buf ^ 1][lane];
-    }
-    for (int w = WARPS - 1; w > warp; --w) D = apply(sm.maps[buf][w][lane], D);
-    if (blocks == 1 && warp == 0) {
-      carry = apply(sm.maps[buf][0][lane], D);
-      if (half == 0) sm.carry[buf][lane] = carry;
-    }
-    if (left > 0) {
-      h = reinterpret_cast<const float2*>(sm.states[buf][warp])[lane];
-      for (int w = warp / TILE_WARPS * TILE_WARPS; w < warp; ++w) {
-        const float4 m = sm.maps[buf][w][lane];
-        h = __ffma2_rn(make_float2(m.x, m.y), h, sm.h[buf][w][lane]);
-      }
-      if (half) h = __ffma2_rn(oa, h, oh);
-      else D = __ffma2_rn(oa, D, oD);
-      T* const dx = dx0 + (long long)(k + half * ROWS) * dx_step + 2 * lane;
-      T* const dr = dr0 + (long long)(k + half * ROWS) * dr_step + 2 * lane;
-      T* const dg = dg0 + (long long)(k + half * ROWS) * dg_step + 2 * lane;
-      float2 G[ROWS];
-#pragma unroll
-      for (int j = ROWS - 1; j >= 0; --j) {
-        G[j] = __fadd2_rn(D, lane_pair(dy + j * Lay::CHANNELS, lane));
-        D = __fmul2_rn(qa[j], G[j]);
-      }
+      };
+      // of each row: a, σ(g), and (s, β) for channels near 1, (σ(r), 1 − a²) otherwise
+      float2 qa[ROWS], qg[ROWS], qs[ROWS], qb[ROWS];
+      float2 a = two(1.0f), h = two(0.0f), D = two(0.0f);
+      if (left > 0) {
+        if (left < Lay::WARP_ROWS) {
+          // a position past the end has r = −∞, x = 0 and dy = 0
+          if constexpr (!ACT8) {
+            T* const to = (T*)rows0 + buf * 3 * ARRAY;
+            fill_rows<T, Lay>(to, wl, left, 0.0f);
+            fill_rows<T, Lay>(to + ARRAY, wl, left, -INFINITY);
+            fill_rows<T, Lay>(to + 2 * ARRAY, wl, left, 0.0f);
+          }
+          fill_rows<T, Lay>(dy0 + buf * DY, wl, left, 0.0f);
+          __syncwarp();
+        }
 #pragma unroll
         for (int j = 0; j < ROWS; ++j) {
-          const float2 x = value(0, j), sgx = __fmul2_rn(qg[j], x);
-          float2 sr, beta, nv;      // nv = −σ(r) / β
+          const float2 x = value(0, j), r = value(1, j), g = value(2, j);
+          float2 beta;
           if constexpr (NEAR) {
-            sr = __fmul2_rn(qs[j], qs[j]);
-            beta = qb[j];
-            nv = __fmul2_rn(qs[j], __fmul2_rn(nscale, near_beta_inverse(__fmul2_rn(sr, rate2))));
+            const float2 d = sigmoid_den(r);
+            qs[j] = make_float2(rsqrt_approx(d.x), rsqrt_approx(d.y));
+            const float2 l2 = __fmul2_rn(__fmul2_rn(qs[j], qs[j]), rate2);
+            qa[j] = near_decay(l2);
+            qb[j] = beta = __fmul2_rn(__fmul2_rn(qs[j], scale), near_beta(l2));
+            qg[j] = sigmoid2(g);
           } else {
-            // 0 where the gate is closed (or u subnormal), as is the limit of all that it is part of
-            const float2 rb = make_float2(qb[j].x < TINY ? 0.0f : rsqrt_approx(qb[j].x), qb[j].y < TINY ? 0.0f : rsqrt_approx(qb[j].y));
-            sr = make_float2(qb[j].x < TINY ? 0.0f : qs[j].x, qb[j].y < TINY ? 0.0f : qs[j].y);
-            beta = __fmul2_rn(qb[j], rb);
-            nv = __fmul2_rn(__fmul2_rn(sr, rb), two(-1.0f));
+            const Gates q = gates2(r, g, rate2);
+            qa[j] = q.a;
+            qg[j] = q.sg;
+            qs[j] = q.sr;
+            qb[j] = q.u;
+            beta = make_float2(sqrt_approx(q.u.x), sqrt_approx(q.u.y));
           }
-          const float2 vdx = __fmul2_rn(G[j], __fmul2_rn(beta, qg[j]));
-          const float2 vdg = __fmul2_rn(__fmul2_rn(vdx, x), __ffma2_rn(qg[j], two(-1.0f), two(1.0f)));
-          // d(log a) σ(r) = G a (h σ(r) − σ(g) x a σ(r) / β)
-          const float2 t = __ffma2_rn(sgx, __fmul2_rn(qa[j], nv), __fmul2_rn(h, sr));
-          const float2 dls = __fmul2_rn(__fmul2_rn(G[j], qa[j]), t);
-          dlam = __fadd2_rn(dlam, dls);
-          const float2 vdr = __fmul2_rn(__fmul2_rn(dls, rate), __ffma2_rn(sr, two(-1.0f), two(1.0f)));
-          h = __ffma2_rn(qa[j], h, __fmul2_rn(beta, sgx));
-          store_lane<WIDE>(row_at(dx, dx_step, j), j, mine, lane, cols, vdx);
-          store_lane<WIDE>(row_at(dr, dr_step, j), j, mine, lane, cols, vdr);
-          store_lane<WIDE>(row_at(dg, dg_step, j), j, mine, lane, cols, vdg);
+          h = __ffma2_rn(qa[j], h, __fmul2_rn(beta, __fmul2_rn(qg[j], x)));
+          a = j == 0 ? qa[j] : __fmul2_rn(a, qa[j]);
+        }
+#pragma unroll
+        for (int j = ROWS - 1; j >= 0; --j) D = __fmul2_rn(qa[j], __fadd2_rn(D, lane_pair(dy + j * Lay::CHANNELS, lane)));
       }
+      const float2 oa = other_half(a), oh = other_half(h), oD = other_half(D);
+      if (half == 0) {
+        const float4 map = after(make_float4(a.x, a.y, D.x, D.y), make_float4(oa.x, oa.y, oD.x, oD.y));
+        sm.maps[buf][warp][lane] = map;
+        sm.h[buf][warp][lane] = __ffma2_rn(oa, h, oh);
+      }
+      __syncthreads();
+      if (blocks > 1) {
+        float4 tile = sm.maps[buf][WARPS - 1][lane];
+#pragma unroll
+        for (int w = WARPS - 2; w >= 0; --w) tile = after(sm.maps[buf][w][lane], tile);
+        D = through_cluster<BL>(box + buf * blocks * BL, tile, warp * 2 + half, WARPS * 2, lane, rank, blocks, carry);
+      } else {
+        D = round == 0 ? carry : sm.carry[buf ^ 1][lane];
+      }
+      for (int w = WARPS - 1; w > warp; --w) D = apply(sm.maps[buf][w][lane], D);
+      if (blocks == 1 && warp == 0) {
+        carry = apply(sm.maps[buf][0][lane], D);
+        if (half == 0) sm.carry[buf][lane] = carry;
+      }
+      if (left > 0) {
+        h = reinterpret_cast<const float2*>(sm.states[buf][warp])[lane];
+        for (int w = warp / TILE_WARPS * TILE_WARPS; w < warp; ++w) {
+          const float4 m = sm.maps[buf][w][lane];
+          h = __ffma2_rn(make_float2(m.x, m.y), h, sm.h[buf][w][lane]);
+        }
+        if (half) h = __ffma2_rn(oa, h, oh);
+        else D = __ffma2_rn(oa, D, oD);
+        T* const dx = dx0 + (long long)(k + half * ROWS) * dx_step + 2 * lane;
+        T* const dr = dr0 + (long long)(k + half * ROWS) * dr_step + 2 * lane;
+        T* const dg = dg0 + (long long)(k + half * ROWS) * dg_step + 2 * lane;
+        float2 G[ROWS];
+#pragma unroll
+        for (int j = ROWS - 1; j >= 0; --j) {
+          G[j] = __fadd2_rn(D, lane_pair(dy + j * Lay::CHANNELS, lane));
+          D = __fmul2_rn(qa[j], G[j]);
+        }
+#pragma unroll
+          for (int j = 0; j < ROWS; ++j) {
+            const float2 x = value(0, j), sgx = __fmul2_rn(qg[j], x);
+            float2 sr, beta, nv;      // nv = −σ(r) / β
+            if constexpr (NEAR) {
+              sr = __fmul2_rn(qs[j], qs[j]);
+              beta = qb[j];
+              nv = __fmul2_rn(qs[j], __fmul2_rn(nscale, near_beta_inverse(__fmul2_rn(sr, rate2))));
+            } else {
+              // 0 where the gate is closed (or u subnormal), as is the limit of all that it is part of
+              const float2 rb = make_float2(qb[j].x < TINY ? 0.0f : rsqrt_approx(qb[j].x), qb[j].y < TINY ? 0.0f : rsqrt_approx(qb[j].y));
+              sr = make_float2(qb[j].x < TINY ? 0.0f : qs[j].x, qb[j].y < TINY ? 0.0f : qs[j].y);
+              beta = __fmul2_rn(qb[j], rb);
+              nv = __fmul2_rn(__fmul2_rn(sr, rb), two(-1.0f));
+            }
+            const float2 vdx = __fmul2_rn(G[j], __fmul2_rn(beta, qg[j]));
+            const float2 vdg = __fmul2_rn(__fmul2_rn(vdx, x), __ffma2_rn(qg[j], two(-1.0f), two(1.0f)));
+            // d(log a) σ(r) = G a (h σ(r) − σ(g) x a σ(r) / β)
+            const float2 t = __ffma2_rn(sgx, __fmul2_rn(qa[j], nv), __fmul2_rn(h, sr));
+            const float2 dls = __fmul2_rn(__fmul2_rn(G[j], qa[j]), t);
+            dlam = __fadd2_rn(dlam, dls);
+            const float2 vdr = __fmul2_rn(__fmul2_rn(dls, rate), __ffma2_rn(sr, two(-1.0f), two(1.0f)));
+            h = __ffma2_rn(qa[j], h, __fmul2_rn(beta, sgx));
+            store_lane<WIDE>(row_at(dx, dx_step, j), j, mine, lane, cols, vdx);
+            store_lane<WIDE>(row_at(dr, dr_step, j), j, mine, lane, cols, vdr);
+            store_lane<WIDE>(row_at(dg, dg_step, j), j, mine, lane, cols, vdg);
+        }
+      }
+      __syncwarp();            // the warp has read its rows: their buffer takes the tile after the next
+      load(wide_tag, buf, k - 2 * span);
     }
-    __syncwarp();            // the warp has read its rows: their buffer takes the tile after the next
-    load(wide_tag, buf, k - 2 * span);
-  }
   };
   if (wide) {
     if (near) walk(std::true_type(), std::bool_constant<VEC>());
@@ -278,22 +278,26 @@ __global__ void __launch_bounds__(WARPS * 32, (sizeof(T) == 2 || WARPS == 8 ? 16
   }
 }
 
-// dlam from the blocks' shares, [rows][width]: 8 threads a channel take every
-// eighth row each, and their sums are added in order.
-__global__ void __launch_bounds__(256) gated_dlam_kernel(const float* part, int rows, int width, const float* lam, int E,
-                                                         float* dlam) {
+// Sums of the blocks' shares of dlam, [rows][width]: a block takes 32 channels
+// of `per` rows, 8 threads a channel every eighth of them, and their sums are
+// added in order.  Into out[blockIdx.y][width], or where lam is given into
+// dlam, times its derivative.
+constexpr int DLAM_ROWS = 1024;     // rows of a block; more are summed in two launches
+__global__ void __launch_bounds__(256) gated_dlam_kernel(const float* part, int rows, int per, int width, const float* lam,
+                                                         int E, float* out) {
   __shared__ float sum[8][32];
   const int c = threadIdx.x & 31, w = threadIdx.x >> 5, e = blockIdx.x * 32 + c;
+  const int from = blockIdx.y * per, to = min(rows, from + per);
   float s = 0.0f;
 #pragma unroll 4
-  for (int i = w; i < rows; i += 8) s += part[(size_t)i * width + e];
+  for (int i = from + w; i < to; i += 8) s += part[(size_t)i * width + e];
   sum[w][c] = s;
   __syncthreads();
-  if (w == 0 && e < E) {
+  if (w != 0) return;
 #pragma unroll
-    for (int k = 1; k < 8; ++k) s += sum[k][c];
-    dlam[e] = s * (-R2L_GATED_RATE / (1.0f + expf(-lam[e])));
-  }
+  for (int k = 1; k < 8; ++k) s += sum[k][c];
+  if (!lam) out[(size_t)blockIdx.y * width + e] = s;
+  else if (e < E) out[e] = s * (-R2L_GATED_RATE / (1.0f + expf(-lam[e])));
 }
 
 }  // namespace gated

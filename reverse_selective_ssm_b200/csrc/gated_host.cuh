@@ -32,9 +32,10 @@ inline bool aligned(const void* p, size_t a) { return ((uintptr_t)p & (a - 1)) =
 inline bool valid_dims(const r2l_dims* d, int B, int L) {
   return d && B > 0 && L > 0 && d->d_inner > 0 && (d->dtype == R2L_BF16 || d->dtype == R2L_FP32);
 }
-// Sizes whose byte counts stay far inside 64 bits, and padded widths inside 32.
+// Sizes whose byte counts stay far inside 64 bits, and padded widths and
+// positions a few rounds past the end inside 32.
 inline bool fits(int B, int L, int E) {
-  return E <= (1 << 30) && (double)B * L * E <= (double)(1ll << 50);
+  return E <= (1 << 30) && L <= (1 << 30) && (double)B * L * E <= (double)(1ll << 50);
 }
 inline size_t elem_bytes(r2l_dtype t) { return t == R2L_BF16 ? 2 : 4; }
 

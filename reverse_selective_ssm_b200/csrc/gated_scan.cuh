@@ -6,15 +6,23 @@
 //   G_k = dy_k + D_k,  D_{k−1} = a_k G_k   (D after the last position: dh_last)
 //
 // Both recurrences are affine maps of one number per channel, so a run of
-// positions is one pair (A, B): out = A · in + B.  A block owns 64 channels of
-// a sequence and takes 64 positions (a tile) at a time: every warp turns its
-// share of the rows into a pair, the pairs of the warps before it give the
-// value that enters the warp, and each row's result follows from it.  The rows
-// of the next tile are on their way to shared memory meanwhile.  Where there
-// are too few channels to fill the SMs, up to 8 blocks of a cluster take 8
-// consecutive tiles at once and swap their tiles' pairs through distributed
-// shared memory, one cluster barrier per 8 tiles: inputs are read once,
-// whatever the split.
+// positions is one pair (A, B): out = A · in + B.  A block owns 32 or 64
+// channels of a sequence.  Its warps take 8 or 16 consecutive positions each;
+// a warp turns its rows into one pair while it waits for nothing, then gets the
+// state that enters from the warp before, hands on the one that leaves and
+// writes its rows.  The rows of the warp's next two turns are on their way to
+// shared memory meanwhile.  Where there are too few channels to fill the SMs,
+// up to 8 blocks of a cluster take consecutive tiles at once and swap their
+// tiles' pairs through distributed shared memory, one cluster barrier a round:
+// inputs are read once, whatever the split.
+//
+// What bounds it (B200, bf16, 8 sequences of 4096 positions, 4096 channels):
+// 8 bytes per position and channel, 164 us at the measured copy rate, against
+// 34 instructions (of which 4 are special functions) per 32 of them.  The scan
+// takes 183 us (5.9 TB/s); under a sustained load that brings the SM clock down
+// to 1.57 GHz, 220 us.  In fp32 (8 x 2048 x 4096) it takes 168 us, 6.4 TB/s.
+// 16 warps an SM at 128 registers beat 28 at 72 (184 and 194 us): the eight
+// rows of a thread overlap each other's special functions.
 #pragma once
 
 #include <cuda_runtime.h>
@@ -273,10 +281,6 @@ __device__ __forceinline__ T* row_at(T* p, int step, int j) {
   return p + (long long)step * j;
 }
 
-__device__ __forceinline__ void store_whole_pair(float* at, float2 v) { *reinterpret_cast<float2*>(at) = v; }
-__device__ __forceinline__ void store_whole_pair(bf16* at, float2 v) {
-  *reinterpret_cast<__nv_bfloat162*>(at) = __float22bfloat162_rn(v);
-}
 __device__ __forceinline__ void store_if(uint16_t* at, int j, int rows, uint16_t v) {
   asm volatile("{\n\t.reg .pred p;\n\tsetp.lt.s32 p, %0, %1;\n\t@p st.global.b16 [%2], %3;\n\t}" ::"r"(j), "r"(rows), "l"(at),
                "h"(v)
@@ -290,6 +294,16 @@ __device__ __forceinline__ uint32_t lane_abs_max(const float* row, int lane) {
 __device__ __forceinline__ uint32_t lane_abs_max(const bf16* row, int lane) {
   const uint32_t w = reinterpret_cast<const uint32_t*>(row)[lane] & 0x7fff7fffu;
   return max(w, w << 16) & 0xffff0000u;
+}
+
+// What an 8-bit checkpoint holds of values that need not be finite: a gate at
+// ±∞ is kept as ±256, where its sigmoid is 0 or 1 just the same; other
+// infinities become NaN.
+__device__ __forceinline__ float storable(float v, bool gate) {
+  return gate && fabsf(v) == INFINITY ? copysignf(256.0f, v) : act8::nan_if_not_finite(v);
+}
+__device__ __forceinline__ float2 storable(float2 v, bool gate) {
+  return make_float2(storable(v.x, gate), storable(v.y, gate));
 }
 
 // A lane's two channels at `at`, where j < rows (as a predicate, not a branch).
@@ -397,11 +411,10 @@ __device__ __forceinline__ float2 through_cluster(float4* box, float4 mine, int 
   return enters;
 }
 
-// A warp's arrival at named barrier `id` of it and the warp that waits there:
-// what it wrote before, the other reads after.  The barrier 0 of __syncthreads
-// is one of them, so the two kinds do not mix within a loop.
-__device__ __forceinline__ void pass_to(int id) { asm volatile("barrier.cta.arrive %0, 64;" ::"r"(id) : "memory"); }
-__device__ __forceinline__ void wait_at(int id) { asm volatile("barrier.cta.sync %0, 64;" ::"r"(id) : "memory"); }
+// A warp's arrival at the named barrier at which `warp` waits (it alone):
+// what it wrote before, the other reads after.  Barrier 0 is __syncthreads'.
+__device__ __forceinline__ void pass_to(int warp) { asm volatile("barrier.cta.arrive %0, 64;" ::"r"(1 + warp) : "memory"); }
+__device__ __forceinline__ void wait_at(int warp) { asm volatile("barrier.cta.sync %0, 64;" ::"r"(1 + warp) : "memory"); }
 
 // The other half warp's value.
 __device__ __forceinline__ float2 other_half(float2 v) {
@@ -412,8 +425,7 @@ __device__ __forceinline__ float2 other_half(float2 v) {
 
 constexpr int ROWS = 8;      // consecutive rows of a thread
 
-// In shared memory, behind it the maps of the block's warps, [2][WARPS][LANES],
-// and of the cluster's blocks, [2][blocks][LANES].
+// In shared memory, behind it the maps of the cluster's blocks, [2][blocks][LANES].
 template <typename T, int LANES, int WARPS>
 struct FwdSmem {
   T in[2][3][WARPS * Layout<T, LANES, ROWS>::WARP_STRIDE];
@@ -488,119 +500,118 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
   if (blocks > 1) cluster_sync();   // every block of the cluster runs before its shared memory is written
 
   auto scan = [&](auto near_tag, auto wide_tag) {
-  constexpr bool NEAR = decltype(near_tag)::value, WIDE = decltype(wide_tag)::value;
-  int k = k0;              // this warp's first position
-  for (int round = 0; round < rounds; ++round, k += span) {
-    const int buf = round & 1, left = n - k;      // positions from this warp's first one to the end
-    const T* const in = rows0 + buf * 3 * ARRAY + half * Lay::GROUP_STRIDE;
-    copies_wait<1>();
-    __syncwarp();
-    float2 P[ROWS], H[ROWS];     // row j's state is P[j] · (state that enters the group) + H[j]
-    float2 a = two(1.0f), h = two(0.0f);
-    if (left > 0) {
-      if (left < Lay::WARP_ROWS) {
-        // A position past the end has r = −∞ and x = 0: a = 1, b = 0, and no
-        // other test is needed in the arithmetic.
-        T* const to = rows0 + buf * 3 * ARRAY;
-        fill_rows<T, Lay>(to, wl, left, 0.0f);
-        fill_rows<T, Lay>(to + ARRAY, wl, left, -INFINITY);
-        fill_rows<T, Lay>(to + 2 * ARRAY, wl, left, 0.0f);
-        __syncwarp();
-      }
-      if constexpr (MODE == 2) {
-        // 8-bit copies: the channels that share a scale are one row of the
-        // warp.  Lane 8i + j gets the largest magnitude of row j of array i and
-        // works out that row's scale; the row's lanes have it by a shuffle.
-        const size_t at = ((size_t)b * strips + e0 / Lay::CHANNELS) * p.L + k;
-        uint32_t top = 0;
+    constexpr bool NEAR = decltype(near_tag)::value, WIDE = decltype(wide_tag)::value;
+    int k = k0;              // this warp's first position
+    for (int round = 0; round < rounds; ++round, k += span) {
+      const int buf = round & 1, left = n - k;      // positions from this warp's first one to the end
+      const T* const in = rows0 + buf * 3 * ARRAY + half * Lay::GROUP_STRIDE;
+      copies_wait<1>();
+      __syncwarp();
+      float2 P[ROWS], H[ROWS];     // row j's state is P[j] · (state that enters the group) + H[j]
+      float2 a = two(1.0f), h = two(0.0f);
+      if (left > 0) {
+        if (left < Lay::WARP_ROWS) {
+          // A position past the end has r = −∞ and x = 0: a = 1, b = 0, and no
+          // other test is needed in the arithmetic.
+          T* const to = rows0 + buf * 3 * ARRAY;
+          fill_rows<T, Lay>(to, wl, left, 0.0f);
+          fill_rows<T, Lay>(to + ARRAY, wl, left, -INFINITY);
+          fill_rows<T, Lay>(to + 2 * ARRAY, wl, left, 0.0f);
+          __syncwarp();
+        }
+        if constexpr (MODE == 2) {
+          // 8-bit copies: the channels that share a scale are one row of the
+          // warp.  Lane 8i + j gets the largest magnitude of row j of array i and
+          // works out that row's scale; the row's lanes have it by a shuffle.
+          const size_t strip = (size_t)b * strips + e0 / Lay::CHANNELS;
+          uint32_t top = 0;
 #pragma unroll
-        for (int i = 0; i < 3; ++i)
+          for (int i = 0; i < 3; ++i)
 #pragma unroll
-          for (int j = 0; j < ROWS; ++j) {
-            const uint32_t m = __reduce_max_sync(0xffffffffu, lane_abs_max(in + i * ARRAY + j * Lay::CHANNELS, lane));
-            if (lane == i * ROWS + j) top = m;
-          }
-        const bool odd = __any_sync(0xffffffffu, top >= 0x7f800000u);
-        if (odd) {   // an infinity or a NaN does not count for the scale
+            for (int j = 0; j < ROWS; ++j) {
+              const uint32_t m = __reduce_max_sync(0xffffffffu, lane_abs_max(in + i * ARRAY + j * Lay::CHANNELS, lane));
+              if (lane == i * ROWS + j) top = m;
+            }
+          const bool odd = __any_sync(0xffffffffu, top >= 0x7f800000u);
+          if (odd) {
 #pragma unroll 1
-          for (int c = 0; c < 3 * ROWS; ++c) {
-            const float2 v = lane_pair(in + c / ROWS * ARRAY + c % ROWS * Lay::CHANNELS, lane);
-            const uint32_t m = __reduce_max_sync(0xffffffffu, max(act8::finite_abs_bits(v.x), act8::finite_abs_bits(v.y)));
-            if (lane == c) top = m;
+            for (int c = 0; c < 3 * ROWS; ++c) {
+              const float2 v = storable(lane_pair(in + c / ROWS * ARRAY + c % ROWS * Lay::CHANNELS, lane), c >= ROWS);
+              const uint32_t m = __reduce_max_sync(0xffffffffu, max(act8::finite_abs_bits(v.x), act8::finite_abs_bits(v.y)));
+              if (lane == c) top = m;
+            }
+          }
+          const uint32_t byte = act8::scale_byte(top);
+          const float down = act8::scale_down(byte);
+          if (lane < 3 * ROWS && lane % ROWS < left)
+            p.ck.scales[0][lane / ROWS * (p.ck.scales[1] - p.ck.scales[0]) + strip * p.ck.Lp + k + lane % ROWS] = (uint8_t)byte;
+#pragma unroll
+          for (int i = 0; i < 3; ++i) {
+            uint16_t* const q = reinterpret_cast<uint16_t*>(p.ck.q[i] + (strip * p.L + k) * STRIP) + lane;
+#pragma unroll
+            for (int j = 0; j < ROWS; ++j) {
+              float2 v = lane_pair(in + i * ARRAY + j * Lay::CHANNELS, lane);
+              if (odd) v = storable(v, i > 0);
+              v = __fmul2_rn(v, two(__shfl_sync(0xffffffffu, down, i * ROWS + j)));
+              store_if(q + j * (STRIP / 2), j, left, act8::to_e4m3x2(v.x, v.y));
+            }
           }
         }
-        const uint32_t byte = act8::scale_byte(top);
-        const float down = act8::scale_down(byte);
-        if (lane < 3 * ROWS && lane % ROWS < left)
-          p.ck.scales[0][lane / ROWS * (p.ck.scales[1] - p.ck.scales[0]) + (size_t)(at / p.L) * p.ck.Lp + k + lane % ROWS] = (uint8_t)byte;
 #pragma unroll
-        for (int i = 0; i < 3; ++i) {
-          uint16_t* const q = reinterpret_cast<uint16_t*>(p.ck.q[i] + at * STRIP) + lane;
-#pragma unroll
-          for (int j = 0; j < ROWS; ++j) {
-            float2 v = lane_pair(in + i * ARRAY + j * Lay::CHANNELS, lane);
-            if (odd) v = make_float2(act8::nan_if_not_finite(v.x), act8::nan_if_not_finite(v.y));
-            v = __fmul2_rn(v, two(__shfl_sync(0xffffffffu, down, i * ROWS + j)));
-            store_if(q + j * (STRIP / 2), j, left, act8::to_e4m3x2(v.x, v.y));
-          }
+        for (int j = 0; j < ROWS; ++j) {
+          float2 aj, bj;
+          coefficients<NEAR>(lane_pair(in + j * Lay::CHANNELS, lane), lane_pair(in + ARRAY + j * Lay::CHANNELS, lane),
+                             lane_pair(in + 2 * ARRAY + j * Lay::CHANNELS, lane), rate2, scale, aj, bj);
+          a = j == 0 ? aj : __fmul2_rn(a, aj);
+          h = j == 0 ? bj : __ffma2_rn(aj, h, bj);
+          P[j] = a;
+          H[j] = h;
         }
       }
-#pragma unroll
-      for (int j = 0; j < ROWS; ++j) {
-        float2 aj, bj;
-        coefficients<NEAR>(lane_pair(in + j * Lay::CHANNELS, lane),
-                                                lane_pair(in + ARRAY + j * Lay::CHANNELS, lane),
-                                                lane_pair(in + 2 * ARRAY + j * Lay::CHANNELS, lane), rate2, scale, aj, bj);
-        a = j == 0 ? aj : __fmul2_rn(a, aj);
-        h = j == 0 ? bj : __ffma2_rn(aj, h, bj);
-        P[j] = a;
-        H[j] = h;
+      // the warp's map, and what its first half's does to the second half
+      float4 map = make_float4(a.x, a.y, h.x, h.y), before = make_float4(1.0f, 1.0f, 0.0f, 0.0f);
+      if (Lay::GROUPS == 2) {
+        const float2 oa = other_half(a), oh = other_half(h);
+        const float4 o = make_float4(oa.x, oa.y, oh.x, oh.y);
+        if (half) before = o;
+        map = after(half ? map : o, half ? o : map);
       }
-    }
-    // the warp's map, and what its first half's does to the second half
-    float4 map = make_float4(a.x, a.y, h.x, h.y), before = make_float4(1.0f, 1.0f, 0.0f, 0.0f);
-    if (Lay::GROUPS == 2) {
-      const float2 oa = other_half(a), oh = other_half(h);
-      const float4 o = make_float4(oa.x, oa.y, oh.x, oh.y);
-      if (half) before = o;
-      map = after(half ? map : o, half ? o : map);
-    }
-    if (blocks > 1 && half == 0) sm.maps[buf][warp][lane] = map;
-    __syncwarp();            // the warp has read its rows: their buffer takes the tile after the next
-    load(wide_tag, buf, k + 2 * span);
-    float2 enters;           // the value that enters this warp
-    if (blocks == 1) {
-      // from warp to warp, and from the last one to the first one's next rows
-      if (round == 0 && warp == 0) {
-        enters = carry;
+      if (blocks > 1 && half == 0) sm.maps[buf][warp][lane] = map;
+      __syncwarp();            // the warp has read its rows: their buffer takes the tile after the next
+      load(wide_tag, buf, k + 2 * span);
+      float2 enters;           // the value that enters this warp
+      if (blocks == 1) {
+        // from warp to warp, and from the last one to the first one's next rows
+        if (round == 0 && warp == 0) {
+          enters = carry;
+        } else {
+          wait_at(warp);
+          enters = sm.carry[warp][lane];
+        }
+        carry = apply(map, enters);
+        if (round + 1 < rounds || warp + 1 < WARPS) {
+          const int next = (warp + 1) % WARPS;
+          if (half == 0) sm.carry[next][lane] = carry;
+          __syncwarp();
+          pass_to(next);
+        }
       } else {
-        wait_at(warp);
-        enters = sm.carry[warp][lane];
-      }
-      carry = apply(map, enters);
-      if (round + 1 < rounds || warp + 1 < WARPS) {
-        const int next = (warp + 1) % WARPS;
-        if (half == 0) sm.carry[next][lane] = carry;
-        __syncwarp();
-        pass_to(next);
-      }
-    } else {
-      __syncthreads();
-      float4 tile = sm.maps[buf][0][lane];
+        __syncthreads();
+        float4 tile = sm.maps[buf][0][lane];
 #pragma unroll
-      for (int w = 1; w < WARPS; ++w) tile = after(sm.maps[buf][w][lane], tile);
-      enters = through_cluster<LANES>(box + buf * blocks * LANES, tile, warp * Lay::GROUPS + half, WARPS * Lay::GROUPS, lane,
-                                      rank, blocks, carry);
-      for (int w = 0; w < warp; ++w) enters = apply(sm.maps[buf][w][lane], enters);
+        for (int w = 1; w < WARPS; ++w) tile = after(sm.maps[buf][w][lane], tile);
+        enters = through_cluster<LANES>(box + buf * blocks * LANES, tile, warp * Lay::GROUPS + half, WARPS * Lay::GROUPS, lane,
+                                        rank, blocks, carry);
+        for (int w = 0; w < warp; ++w) enters = apply(sm.maps[buf][w][lane], enters);
+      }
+      if (MODE >= 1 && k % TILE == 0 && half == 0 && left > 0)
+        reinterpret_cast<float2*>(p.ck.states + ((size_t)b * p.ck.tiles + k / TILE) * p.strips * STRIP + e0)[lane] = enters;
+      if (Lay::GROUPS == 2) enters = apply(before, enters);
+      T* const out = y0 + (long long)(k + half * ROWS) * y_step + 2 * lane;
+#pragma unroll
+      for (int j = 0; j < ROWS; ++j)
+        store_lane<WIDE>(row_at(out, y_step, j), j, left - half * ROWS, lane, cols, __ffma2_rn(P[j], enters, H[j]));
     }
-    if (MODE >= 1 && k % TILE == 0 && half == 0 && left > 0)
-      reinterpret_cast<float2*>(p.ck.states + ((size_t)b * p.ck.tiles + k / TILE) * p.strips * STRIP + e0)[lane] = enters;
-    if (Lay::GROUPS == 2) enters = apply(before, enters);
-    T* const out = y0 + (long long)(k + half * ROWS) * y_step + 2 * lane;
-#pragma unroll
-    for (int j = 0; j < ROWS; ++j)
-      store_lane<WIDE>(row_at(out, y_step, j), j, left - half * ROWS, lane, cols, __ffma2_rn(P[j], enters, H[j]));
-  }
   };
   if (wide) {
     if (near) scan(std::true_type(), std::bool_constant<VEC>());

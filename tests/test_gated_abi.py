@@ -53,6 +53,7 @@ def test_forward_refusals(lib):
     assert _fwd(lib, dims=_dims(dtype=torch.float32), g=FAKE + 130) == 3
     for name in ("lam", "h0", "h_last", "lengths", "status"):
         assert _fwd(lib, **{name: FAKE + 2}) == 3
+    assert _fwd(lib, L=2 ** 30 + 1) == 2
     assert _fwd(lib, dims=_dims(E=2 ** 31 - 1), B=65536, L=65536, **{n: 2 ** 31 - 1 for n in ("ldx", "ldr", "ldg", "ldy")}) == 2
 
 
@@ -67,7 +68,10 @@ def test_checkpoint_sizes(lib):
     assert bd.gated_scan_checkpoint_size(_dims(E=2 ** 20), 2 ** 31 - 1, 2 ** 31 - 1) == 0
     assert bd.gated_scan_checkpoint_size(d, 1, 0) == 0
     assert bd.gated_scan_checkpoint_size(_dims(E=-1), 1, 1) == 0
+    assert bd.gated_scan_checkpoint_size(_dims(E=2), 1, 2 ** 30 + 1) == 0
     assert bd.gated_scan_backward_workspace_size(d, 3, 129) >= 3 * 100 * 4
+    n = bd.gated_scan_backward_workspace_size(d, 2000, 1)           # sums of more than 1024 rows lie behind them
+    assert n >= (2000 + 2) * 128 * 4
     assert bd.gated_scan_backward_workspace_size(d, 3, 0) == 0
     # serving setup: half the bytes of x, r and g in bf16, and the states
     big = bd.gated_scan_checkpoint_size(_dims(E=4096, flags=bd.R2L_FLAG_ACT8), 8, 4096)

@@ -345,6 +345,50 @@ def test_extreme_gates(dtype, L):
     check_forward(d, y2, h2, B, L, False)
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("fast", [False, True], ids=["slow", "fast"])
+def test_infinite_gates_in_8_bits(dtype, fast):
+    """±inf in r and g closes and opens gates in the 8-bit checkpoint too: it stands for them by ±256, whose sigmoid is
+    0 (2^-369 in float64, below the flush bound) or 1."""
+    B, L, E = 2, 130, 96
+    d = make(B, L, E, dtype, seed=20)
+    if fast:
+        d["lam"] += 6.0
+    inf = float("inf")
+    d["r"][3::17, ::5], d["r"][5::19, 1::7] = -inf, inf
+    d["g"][4::13, ::3], d["g"][6::11, 1::4] = -inf, inf
+    d["r"][:, 64:] = -inf                                       # a whole group of channels closed throughout
+    y, h, _, out = train(d, dev(d), B, L, E, dtype, False, True)
+    check_forward(d, y, h, B, L, False)
+    for k in ("x", "r", "g"):
+        v = S.to_f64(d[k])
+        d[k + "8"] = torch.from_numpy(O.act8_values(np.where(np.isinf(v), np.copysign(256.0, v), v)))
+    for k, v in out.items():
+        assert bool(torch.isfinite(v.float()).all()), k
+    check_backward(d, out, B, L, False, ("x8", "r8", "g8"))
+
+
+def test_many_sequences():
+    """More sequences than one launch sums dlam over."""
+    B, L, E = 2500, 3, 10
+    d = make(B, L, E, FP32, seed=21, lens=[b % 4 for b in range(B)])
+    y, h, _, out = train(d, dev(d), B, L, E, FP32, False, False)
+    check_forward(d, y, h, B, L, False)
+    check_backward(d, out, B, L, False)
+
+
+def test_final_state_over_the_initial_one():
+    """h_last = h0 in whole scans and training forwards of both block shapes and of a cluster."""
+    for B, L, E in ((2, 100, 64), (2, 700, 96), (1, 2100, 64)):
+        d = make(B, L, E, FP32, seed=22)
+        c = dev(d)
+        dims = bd.gated_dims(E, FP32)
+        for f in (bd.gated_scan, bd.gated_scan_train):
+            state = c["h0"].clone()
+            out = f(c["x"], c["r"], c["g"], c["lam"], dims, B, L, h0=state, h_last=state)
+            check_forward(d, out[0], state, B, L, False)
+
+
 def test_all_positions_closed():
     """Nothing enters: zeros stay zeros exactly, and the adjoint passes through."""
     B, L, E = 2, 100, 64
