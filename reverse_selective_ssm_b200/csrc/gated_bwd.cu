@@ -88,7 +88,7 @@ r2l_status r2l_gated_scan_backward(const r2l_gated_in* in, const void* dy, int l
   p.forward = (dims->flags & R2L_FLAG_FORWARD_SCAN) ? 1 : 0;
   p.lengths = lengths; p.status = (uint32_t*)workspace;
   p.ck = checkpoint_at(k, const_cast<void*>(checkpoint));
-  const bool vec = E % 2 == 0 && (act8 || (rows16(p.x, p.ldx, es) && rows16(p.r, p.ldr, es) && rows16(p.g, p.ldg, es))) &&
+  const bool vec = E * es % 16 == 0 && (act8 || (rows16(p.x, p.ldx, es) && rows16(p.r, p.ldr, es) && rows16(p.g, p.ldg, es))) &&
                    rows16(p.dy, p.ld_dy, es) && rows16(p.dx, p.ld_dx, es) && rows16(p.dr, p.ld_dr, es) &&
                    rows16(p.dg, p.ld_dg, es);
   const Split c = backward_split(dims, B, L);

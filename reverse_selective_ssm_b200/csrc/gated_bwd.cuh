@@ -64,7 +64,8 @@ __global__ void __launch_bounds__(WARPS * 32, (sizeof(T) == 2 || WARPS == 8 ? 16
   const int k0 = (rounds - 1) * span + (int)(blocks - 1 - rank) * SPAN + warp * Lay::WARP_ROWS;
   const long long row0 = (long long)b * p.L + (p.forward ? 0 : n - 1);   // position 0
   const size_t strip = (size_t)b * p.strips + e0 / STRIP;
-  const bool wide = VEC && cols == Lay::CHANNELS;
+  const bool exists = Lay::channel(wl) < cols;       // VEC: this lane's chunk of a row
+  const int c0 = exists ? Lay::channel(wl) : 0;
   const Q* in0[3];          // x, r, g: position 0
   int in_step[3];
   if constexpr (ACT8) {     // rows of 64 bytes in scan order
@@ -85,18 +86,21 @@ __global__ void __launch_bounds__(WARPS * 32, (sizeof(T) == 2 || WARPS == 8 ? 16
   Q* const rows0 = sm.in[0][0] + warp * LayQ::WARP_STRIDE;
   T* const dy0 = sm.dy[0] + warp * Lay::WARP_STRIDE;
 
-  auto load = [&](auto wide_tag, int buf, int k) {
-    constexpr bool WIDE = decltype(wide_tag)::value;
+  auto load = [&](int buf, int k) {
     if (k >= 0 && k < n) {
 #pragma unroll
       for (int i = 0; i < 3; ++i) {
-        if constexpr (WIDE || ACT8)
-          copy_rows<Q, LayQ>(smem_addr(rows0 + (buf * 3 + i) * ARRAY + LayQ::chunk(wl)), in0[i] + LayQ::channel(wl), in_step[i], k, n, wl);
+        Q* const to = rows0 + (buf * 3 + i) * ARRAY;
+        if constexpr (ACT8)
+          copy_rows<Q, LayQ>(smem_addr(to + LayQ::chunk(wl)), in0[i] + LayQ::channel(wl), in_step[i], k, n, wl, true);
+        else if constexpr (VEC)
+          copy_rows<Q, LayQ>(smem_addr(to + LayQ::chunk(wl)), in0[i] + c0, in_step[i], k, n, wl, exists);
         else
-          copy_elements<Q, LayQ>(rows0 + (buf * 3 + i) * ARRAY, in0[i], in_step[i], k, n, cols, wl);
+          copy_elements<Q, LayQ>(to, in0[i], in_step[i], k, n, cols, wl);
       }
-      if constexpr (WIDE) copy_rows<T, Lay>(smem_addr(dy0 + buf * DY + Lay::chunk(wl)), first_dy + Lay::channel(wl), dy_step, k, n, wl);
-      else copy_elements<T, Lay>(dy0 + buf * DY, first_dy, dy_step, k, n, cols, wl);
+      T* const to = dy0 + buf * DY;
+      if constexpr (VEC) copy_rows<T, Lay>(smem_addr(to + Lay::chunk(wl)), first_dy + c0, dy_step, k, n, wl, exists);
+      else copy_elements<T, Lay>(to, first_dy, dy_step, k, n, cols, wl);
       if (wl < BL / 2)
         copy16(smem_addr(sm.states[buf][warp] + 4 * wl), states0 + (long long)(k / TILE) * (p.strips * STRIP) + 4 * wl);
       if (ACT8 && wl < 3) copy16(smem_addr(sm.scales[buf][warp][wl]), p.ck.scales[wl] + strip * p.ck.Lp + k);
@@ -104,8 +108,8 @@ __global__ void __launch_bounds__(WARPS * 32, (sizeof(T) == 2 || WARPS == 8 ? 16
     copies_commit();
   };
   // the first rows are on their way before anything is waited for
-  if (wide) load(std::bool_constant<VEC>(), 0, k0), load(std::bool_constant<VEC>(), 1, k0 - span);
-  else load(std::false_type(), 0, k0), load(std::false_type(), 1, k0 - span);
+  load(0, k0);
+  load(1, k0 - span);
 
   const float2 rate = decay_rates(p.lam + e0, lane, cols), rate2 = __fmul2_rn(rate, two(LOG2E));
   const float2 scale = near_scale(rate2);
@@ -115,8 +119,8 @@ __global__ void __launch_bounds__(WARPS * 32, (sizeof(T) == 2 || WARPS == 8 ? 16
   float2 dlam = two(0.0f);
   if (blocks > 1) cluster_sync();
 
-  auto walk = [&](auto near_tag, auto wide_tag) {
-    constexpr bool NEAR = decltype(near_tag)::value, WIDE = decltype(wide_tag)::value;
+  auto walk = [&](auto near_tag) {
+    constexpr bool NEAR = decltype(near_tag)::value;
     int k = k0;                    // this warp's first position
     for (int round = 0; round < rounds; ++round, k -= span) {
       const int buf = round & 1, left = n - k;     // positions from this warp's first one to the end
@@ -242,22 +246,17 @@ __global__ void __launch_bounds__(WARPS * 32, (sizeof(T) == 2 || WARPS == 8 ? 16
             dlam = __fadd2_rn(dlam, dls);
             const float2 vdr = __fmul2_rn(__fmul2_rn(dls, rate), __ffma2_rn(sr, two(-1.0f), two(1.0f)));
             h = __ffma2_rn(qa[j], h, __fmul2_rn(beta, sgx));
-            store_lane<WIDE>(row_at(dx, dx_step, j), j, mine, lane, cols, vdx);
-            store_lane<WIDE>(row_at(dr, dr_step, j), j, mine, lane, cols, vdr);
-            store_lane<WIDE>(row_at(dg, dg_step, j), j, mine, lane, cols, vdg);
+            store_lane<VEC>(row_at(dx, dx_step, j), j, mine, lane, cols, vdx);
+            store_lane<VEC>(row_at(dr, dr_step, j), j, mine, lane, cols, vdr);
+            store_lane<VEC>(row_at(dg, dg_step, j), j, mine, lane, cols, vdg);
         }
       }
       __syncwarp();            // the warp has read its rows: their buffer takes the tile after the next
-      load(wide_tag, buf, k - 2 * span);
+      load(buf, k - 2 * span);
     }
   };
-  if (wide) {
-    if (near) walk(std::true_type(), std::bool_constant<VEC>());
-    else walk(std::false_type(), std::bool_constant<VEC>());
-  } else {
-    if (near) walk(std::true_type(), std::false_type());
-    else walk(std::false_type(), std::false_type());
-  }
+  if (near) walk(std::true_type());
+  else walk(std::false_type());
   if (p.dh0 && rank == 0 && warp == 0 && half == 0) store_pair<false>(p.dh0 + (size_t)b * p.E + e0, lane, cols, carry);
   for (long long i = n + (long long)(rank * WARPS + warp) * 2 + half; i < p.L; i += blocks * WARPS * 2) {   // rows past the end
     const long long m = (long long)b * p.L + i;

@@ -197,9 +197,11 @@ __device__ __forceinline__ void write_status(const int32_t* lengths, int B, int 
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) { return (uint32_t)__cvta_generic_to_shared(p); }
 
-// 16 bytes to an address of shared memory.
-__device__ __forceinline__ void copy16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+// 16 bytes to an address of shared memory; zeros where they do not exist (src is valid all the same).
+__device__ __forceinline__ void copy16(uint32_t dst, const void* src, bool exists = true) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.eq.u32 p, %2, 0;\n\tcp.async.cg.shared.global [%0], [%1], 16, p;\n\t}" ::"r"(dst),
+               "l"(src), "r"((uint32_t)exists)
+               : "memory");
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int PENDING>
@@ -228,35 +230,41 @@ struct Layout {
   static __device__ __forceinline__ int channel(int wl) { return wl % CHUNKS * PER; }
 };
 
-__device__ __forceinline__ void copy_element(float* to, const float* from) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_addr(to)), "l"(from) : "memory");
+// One element to shared memory, or 0 where it does not exist (`from` is valid all the same).
+__device__ __forceinline__ void copy_element(float* to, const float* from, bool exists) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_addr(to)), "l"(from), "r"(exists ? 4 : 0) : "memory");
 }
-__device__ __forceinline__ void copy_element(bf16* to, const bf16* from) { *to = *from; }
+__device__ __forceinline__ void copy_element(bf16* to, const bf16* from, bool exists) {
+  *to = exists ? *from : from_f32<bf16>(0.0f);
+}
 
 // The rows of a warp from position k on, on their way to dst in shared memory.
 // A warp copies only the rows that it reads itself, so a copy needs no barrier
 // of the block.  `step` leads to the next position.  Rows past the last
 // position n − 1 take that one's values (no test per copy; see fill_rows).
-// copy_rows: rows start on 16-byte boundaries and have all the block's
-// channels; `first` is position 0 at this lane's channel(), `dst` this
-// lane's chunk of the warp's rows: an address is one multiply-add.
+// copy_rows: rows start on 16-byte boundaries and channels come in multiples of
+// them, so a chunk exists or does not; `first` is position 0 at this lane's
+// channel() (any valid one if it does not exist), `dst` this lane's chunk of
+// the warp's rows: an address is one multiply-add.
 template <typename T, typename LAY>
-__device__ __forceinline__ void copy_rows(uint32_t dst, const T* first, int step, int k, int n, int wl) {
+__device__ __forceinline__ void copy_rows(uint32_t dst, const T* first, int step, int k, int n, int wl, bool exists) {
   k += wl / LAY::CHUNKS;
 #pragma unroll
   for (int i = 0; i < LAY::WARP_ROWS; i += LAY::AT_ONCE)
-    copy16(dst + LAY::at(i) * (int)sizeof(T), first + (long long)min(k + i, n - 1) * step);
+    copy16(dst + LAY::at(i) * (int)sizeof(T), first + (long long)min(k + i, n - 1) * step, exists);
 }
 // copy_elements: any rows, of which `cols` channels exist (the others are 0);
 // `first` is position 0 at the block's first channel.
 template <typename T, typename LAY>
 __device__ __forceinline__ void copy_elements(T* dst, const T* first, int step, int k, int n, int cols, int wl) {
+  static_assert(LAY::CHANNELS % 32 == 0, "a lane copies a channel");
+#pragma unroll
+  for (int c = 0; c < LAY::CHANNELS; c += 32) {
+    const bool exists = c + wl < cols;
+    const T* const from = first + (exists ? c + wl : 0);
 #pragma unroll 8
-  for (int i = 0; i < LAY::WARP_ROWS * LAY::CHANNELS; i += 32) {
-    const int row = (i + wl) / LAY::CHANNELS, c = (i + wl) % LAY::CHANNELS;
-    T* const to = dst + LAY::at(row) + c;
-    if (c < cols) copy_element(to, first + (long long)min(k + row, n - 1) * step + c);
-    else *to = from_f32<T>(0.0f);
+    for (int row = 0; row < LAY::WARP_ROWS; ++row)
+      copy_element(dst + LAY::at(row) + c + wl, from + (long long)min(k + row, n - 1) * step, exists);
   }
 }
 // v in all channels of the rows from `rows` on, of a warp that has no more.
@@ -306,29 +314,35 @@ __device__ __forceinline__ float2 storable(float2 v, bool gate) {
   return make_float2(storable(v.x, gate), storable(v.y, gate));
 }
 
+__device__ __forceinline__ void store_if(float* at, int j, int rows, float v) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.lt.s32 p, %0, %1;\n\t@p st.global.f32 [%2], %3;\n\t}" ::"r"(j), "r"(rows), "l"(at),
+               "f"(v)
+               : "memory");
+}
+
 // A lane's two channels at `at`, where j < rows (as a predicate, not a branch).
-// WIDE: both exist, on a boundary of two; else `cols` − 2·lane of them exist.
-template <bool WIDE>
+// VEC: both or none exist, on a boundary of two; else `cols` − 2·lane of them.
+template <bool VEC>
 __device__ __forceinline__ void store_lane(float* at, int j, int rows, int lane, int cols, float2 v) {
-  if constexpr (WIDE) {
+  if constexpr (VEC) {
     asm volatile("{\n\t.reg .pred p;\n\tsetp.lt.s32 p, %0, %1;\n\t@p st.global.v2.f32 [%2], {%3, %4};\n\t}" ::"r"(j),
-                 "r"(rows), "l"(at), "f"(v.x), "f"(v.y)
+                 "r"(2 * lane < cols ? rows : 0), "l"(at), "f"(v.x), "f"(v.y)
                  : "memory");
-  } else if (j < rows) {
-    if (2 * lane < cols) at[0] = v.x;
-    if (2 * lane + 1 < cols) at[1] = v.y;
+  } else {
+    store_if(at, j, 2 * lane < cols ? rows : 0, v.x);
+    store_if(at + 1, j, 2 * lane + 1 < cols ? rows : 0, v.y);
   }
 }
-template <bool WIDE>
+template <bool VEC>
 __device__ __forceinline__ void store_lane(bf16* at, int j, int rows, int lane, int cols, float2 v) {
   const __nv_bfloat162 w = __float22bfloat162_rn(v);
-  if constexpr (WIDE) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.lt.s32 p, %0, %1;\n\t@p st.global.b32 [%2], %3;\n\t}" ::"r"(j), "r"(rows),
-                 "l"(at), "r"(*reinterpret_cast<const uint32_t*>(&w))
+  if constexpr (VEC) {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.lt.s32 p, %0, %1;\n\t@p st.global.b32 [%2], %3;\n\t}" ::"r"(j),
+                 "r"(2 * lane < cols ? rows : 0), "l"(at), "r"(*reinterpret_cast<const uint32_t*>(&w))
                  : "memory");
-  } else if (j < rows) {
-    if (2 * lane < cols) at[0] = w.x;
-    if (2 * lane + 1 < cols) at[1] = w.y;
+  } else {
+    store_if(reinterpret_cast<uint16_t*>(at), j, 2 * lane < cols ? rows : 0, __bfloat16_as_ushort(w.x));
+    store_if(reinterpret_cast<uint16_t*>(at) + 1, j, 2 * lane + 1 < cols ? rows : 0, __bfloat16_as_ushort(w.y));
   }
 }
 
@@ -462,8 +476,8 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
   const int k0 = (int)rank * SPAN + warp * Lay::WARP_ROWS;     // this warp's first position in the first round
   const long long row0 = (long long)b * p.L + (p.forward ? 0 : n - 1);   // position 0
 
-  const bool wide = VEC && cols == Lay::CHANNELS;
-  const int c0 = e0 + (wide ? Lay::channel(wl) : 0);
+  const bool exists = Lay::channel(wl) < cols;       // VEC: this lane's chunk of a row
+  const int c0 = e0 + (VEC && exists ? Lay::channel(wl) : 0);
   const T* const x0 = (const T*)p.x + row0 * p.ldx + c0;
   const T* const r0 = (const T*)p.r + row0 * p.ldr + c0;
   const T* const g0 = (const T*)p.g + row0 * p.ldg + c0;
@@ -473,13 +487,13 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
   T* const rows0 = sm.in[0][0] + warp * Lay::WARP_STRIDE;
 
   const uint32_t chunk0 = smem_addr(rows0 + Lay::chunk(wl));
-  auto load = [&](auto wide_tag, int buf, int k) {
+  auto load = [&](int buf, int k) {
     if (k < n) {
-      if constexpr (decltype(wide_tag)::value) {
+      if constexpr (VEC) {
         const uint32_t to = chunk0 + buf * (3 * ARRAY * (int)sizeof(T));
-        copy_rows<T, Lay>(to, x0, x_step, k, n, wl);
-        copy_rows<T, Lay>(to + ARRAY * (int)sizeof(T), r0, r_step, k, n, wl);
-        copy_rows<T, Lay>(to + 2 * ARRAY * (int)sizeof(T), g0, g_step, k, n, wl);
+        copy_rows<T, Lay>(to, x0, x_step, k, n, wl, exists);
+        copy_rows<T, Lay>(to + ARRAY * (int)sizeof(T), r0, r_step, k, n, wl, exists);
+        copy_rows<T, Lay>(to + 2 * ARRAY * (int)sizeof(T), g0, g_step, k, n, wl, exists);
       } else {
         T* const to = rows0 + buf * 3 * ARRAY;
         copy_elements<T, Lay>(to, x0, x_step, k, n, cols, wl);
@@ -490,8 +504,8 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
     copies_commit();
   };
   // the first rows are on their way before anything is waited for
-  if (wide) load(std::bool_constant<VEC>(), 0, k0), load(std::bool_constant<VEC>(), 1, k0 + span);
-  else load(std::false_type(), 0, k0), load(std::false_type(), 1, k0 + span);
+  load(0, k0);
+  load(1, k0 + span);
 
   const float2 rate2 = __fmul2_rn(decay_rates(p.lam + e0, lane, cols), two(LOG2E));
   const float2 scale = near_scale(rate2);
@@ -499,8 +513,8 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
   float2 carry = p.h0 ? load_vec_pair(p.h0 + (size_t)b * p.E + e0, lane, cols) : two(0.0f);
   if (blocks > 1) cluster_sync();   // every block of the cluster runs before its shared memory is written
 
-  auto scan = [&](auto near_tag, auto wide_tag) {
-    constexpr bool NEAR = decltype(near_tag)::value, WIDE = decltype(wide_tag)::value;
+  auto scan = [&](auto near_tag) {
+    constexpr bool NEAR = decltype(near_tag)::value;
     int k = k0;              // this warp's first position
     for (int round = 0; round < rounds; ++round, k += span) {
       const int buf = round & 1, left = n - k;      // positions from this warp's first one to the end
@@ -578,7 +592,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
       }
       if (blocks > 1 && half == 0) sm.maps[buf][warp][lane] = map;
       __syncwarp();            // the warp has read its rows: their buffer takes the tile after the next
-      load(wide_tag, buf, k + 2 * span);
+      load(buf, k + 2 * span);
       float2 enters;           // the value that enters this warp
       if (blocks == 1) {
         // from warp to warp, and from the last one to the first one's next rows
@@ -610,16 +624,11 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
       T* const out = y0 + (long long)(k + half * ROWS) * y_step + 2 * lane;
 #pragma unroll
       for (int j = 0; j < ROWS; ++j)
-        store_lane<WIDE>(row_at(out, y_step, j), j, left - half * ROWS, lane, cols, __ffma2_rn(P[j], enters, H[j]));
+        store_lane<VEC>(row_at(out, y_step, j), j, left - half * ROWS, lane, cols, __ffma2_rn(P[j], enters, H[j]));
     }
   };
-  if (wide) {
-    if (near) scan(std::true_type(), std::bool_constant<VEC>());
-    else scan(std::false_type(), std::bool_constant<VEC>());
-  } else {
-    if (near) scan(std::true_type(), std::false_type());
-    else scan(std::false_type(), std::false_type());
-  }
+  if (near) scan(std::true_type());
+  else scan(std::false_type());
   if (p.h_last && rank == 0 && warp == WARPS - 1 && half == 0)
     store_pair<false>(p.h_last + (size_t)b * p.E + e0, lane, cols, carry);
 }
