@@ -22,6 +22,15 @@ Split forward_split(int B, int E, int L, int mode) {
   return {mode == 2 ? cluster_of(jobs64, 64, L, 256) : cluster_of((long long)B * ((E - 1) / 32 + 1), 128, L, 190), 8};
 }
 
+// Whether every thread walks a sequence by itself: steps of one or two
+// positions (2 positions of 8 x 1024 channels 3.2 us, in tiles 3.8; 4 positions
+// 4.5 and 3.5), and short pieces of so many channels that tiles, filled by 8
+// positions to a quarter, would take several waves (8192 sequences of 4 x 4096
+// channels 209 us, in tiles 622; 12 positions 192 and 220, 16 195 and 143).
+bool walks(int B, int E, int L) {
+  return L <= 2 || (L <= 16 && (long long)B * ((E - 1) / 64 + 1) > 592);
+}
+
 template <typename T, bool VEC, int MODE, int LANES, int WARPS>
 r2l_status launch_shape(const FwdArgs& p, uint32_t blocks, cudaStream_t st) {
   using namespace r2l::gated;
@@ -37,10 +46,12 @@ r2l_status launch_forward(const FwdArgs& p, Split c, cudaStream_t st) {
 template <typename T, bool VEC>
 r2l_status run_forward(const FwdArgs& p, int mode, cudaStream_t st) {
   using namespace r2l::gated;
-  if (mode == 0 && p.L <= WALK_MAX) {
-    const long long grid = ((long long)p.B * ((p.E + 1) / 2) + 127) / 128;
+  if (mode == 0 && walks(p.B, p.E, p.L)) {
+    const int pairs = (p.E + 1) / 2, threads = pairs <= 32 ? 32 : pairs <= 64 ? 64 : 128;
+    const uint32_t blocks = (uint32_t)((pairs - 1) / threads + 1);
+    const long long grid = (long long)p.B * blocks;
     if (grid > 2147483647LL) return R2L_ERR_UNSUPPORTED;
-    gated_walk_kernel<T, VEC><<<(unsigned)grid, 128, 0, st>>>(p);
+    gated_walk_kernel<T, VEC><<<(unsigned)grid, threads, 0, st>>>(p, blocks);
     R2L_LAUNCH_CHECK();
     return R2L_OK;
   }
