@@ -595,6 +595,8 @@ def gated_scan_backward(dy: torch.Tensor, lam: torch.Tensor, dims: Dims, B: int,
         ws = workspace
         if ws is None:
             ws = torch.empty(gated_scan_backward_workspace_size(dims, B, L), dtype=torch.uint8, device=dev)
+        if dx is None and dr is None and dg is None:
+            out.update(zip(("dx", "dr", "dg"), torch.empty((3, M, E), dtype=dtype, device=dev).unbind(0)))
         for n, t in out.items():
             if t is None:
                 out[n] = torch.empty((M, E), dtype=dtype, device=dev)

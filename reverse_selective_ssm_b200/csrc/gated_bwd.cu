@@ -22,7 +22,8 @@ template <typename T, bool VEC, bool ACT8>
 r2l_status run_backward(const BwdArgs& p, Split c, cudaStream_t st) {
   using namespace r2l::gated;
   const long long jobs = (long long)p.B * ((p.E - 1) / 32 + 1);
-  if (c.warps == 4) return launch(gated_bwd_kernel<T, VEC, ACT8, 4>, p, jobs, c.blocks, 128, bwd_smem_bytes<T, ACT8, 4>(c.blocks), st);
+  if (c.warps == 4)
+    return launch(gated_bwd_kernel<T, VEC, ACT8, 4>, p, jobs, c.blocks, 128, bwd_smem_bytes<T, ACT8, 4>(c.blocks), st);
   return launch(gated_bwd_kernel<T, VEC, ACT8, 8>, p, jobs, c.blocks, 256, bwd_smem_bytes<T, ACT8, 8>(c.blocks), st);
 }
 

@@ -4,7 +4,16 @@
 // the first.  The adjoint of a warp's rows is an affine map of D like their
 // states are of h, with the same product of decays, so one exchange between
 // the warps hands both on: D from the warps (and the cluster's blocks) behind,
-// h from the state saved at the tile's start and the warps before.
+// h from the state saved at the tile's start and the warps before.  A thread
+// keeps its 8 rows' gates in registers between the two.
+//
+// What bounds it (B200, bf16, 8 x 4096 x 4096): 14 bytes per position and
+// channel, 288 us at the measured copy rate, against 72 instructions per 32 of
+// them at 16 warps an SM (the 128 registers of the gates), of which 65% of the
+// issue slots are used: 397 us, 4.8 TB/s.  In fp32 (8 x 2048 x 4096) 313 us,
+// 6.0 TB/s.  From 8-bit rows it reads 3 bytes less and spends 14 instructions
+// more on them: 445 us.  168 registers and 12 warps: 422 us.  Gradients staged
+// in shared memory and written 16 bytes a lane: 407 us.
 #pragma once
 
 #include "gated_scan.cuh"
@@ -233,7 +242,8 @@ __global__ void __launch_bounds__(WARPS * 32, (sizeof(T) == 2 || WARPS == 8 ? 16
               nv = __fmul2_rn(qs[j], __fmul2_rn(nscale, near_beta_inverse(__fmul2_rn(sr, rate2))));
             } else {
               // 0 where the gate is closed (or u subnormal), as is the limit of all that it is part of
-              const float2 rb = make_float2(qb[j].x < TINY ? 0.0f : rsqrt_approx(qb[j].x), qb[j].y < TINY ? 0.0f : rsqrt_approx(qb[j].y));
+              const float2 rb = make_float2(qb[j].x < TINY ? 0.0f : rsqrt_approx(qb[j].x),
+                                            qb[j].y < TINY ? 0.0f : rsqrt_approx(qb[j].y));
               sr = make_float2(qb[j].x < TINY ? 0.0f : qs[j].x, qb[j].y < TINY ? 0.0f : qs[j].y);
               beta = __fmul2_rn(qb[j], rb);
               nv = __fmul2_rn(__fmul2_rn(sr, rb), two(-1.0f));

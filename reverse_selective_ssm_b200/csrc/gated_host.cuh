@@ -106,7 +106,8 @@ r2l_status launch(void (*kern)(Args, uint32_t), const Args& p, long long jobs, u
                   cudaStream_t st) {
   const long long grid = jobs * blocks;
   if (grid > 2147483647LL) return R2L_ERR_UNSUPPORTED;
-  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
+  if (smem > 48 * 1024 &&
+      cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess) {
     (void)cudaGetLastError();
     return R2L_ERR_CUDA;
   }
@@ -120,7 +121,7 @@ r2l_status launch(void (*kern)(Args, uint32_t), const Args& p, long long jobs, u
   attr[0].val.clusterDim.x = blocks;
   attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
   cfg.attrs = attr;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = blocks > 1 ? 1 : 0;
   if (cudaLaunchKernelEx(&cfg, kern, p, blocks) != cudaSuccess) {
     (void)cudaGetLastError();
     return R2L_ERR_CUDA;

@@ -35,7 +35,8 @@ template <typename T, bool VEC, int MODE, int LANES, int WARPS>
 r2l_status launch_shape(const FwdArgs& p, uint32_t blocks, cudaStream_t st) {
   using namespace r2l::gated;
   const long long jobs = (long long)p.B * ((p.E - 1) / (2 * LANES) + 1);
-  return launch(gated_scan_kernel<T, VEC, MODE, LANES, WARPS>, p, jobs, blocks, WARPS * 32, fwd_smem_bytes<T, LANES, WARPS>(blocks), st);
+  return launch(gated_scan_kernel<T, VEC, MODE, LANES, WARPS>, p, jobs, blocks, WARPS * 32,
+                fwd_smem_bytes<T, LANES, WARPS>(blocks), st);
 }
 template <typename T, bool VEC, int MODE>
 r2l_status launch_forward(const FwdArgs& p, Split c, cudaStream_t st) {
@@ -89,7 +90,8 @@ r2l_status forward_impl(const r2l_gated_in* in, void* y, int ldy, float* h_last,
     p.ck = checkpoint_at(k, checkpoint);
   }
   const int mode = !train ? 0 : (dims->flags & R2L_FLAG_ACT8) ? 2 : 1;
-  const bool vec = E * es % 16 == 0 && rows16(p.x, p.ldx, es) && rows16(p.r, p.ldr, es) && rows16(p.g, p.ldg, es) && rows16(p.y, p.ldy, es);
+  const bool vec = E * es % 16 == 0 && rows16(p.x, p.ldx, es) && rows16(p.r, p.ldr, es) && rows16(p.g, p.ldg, es) &&
+                   rows16(p.y, p.ldy, es);
   cudaStream_t st = (cudaStream_t)stream;
   if (dims->dtype == R2L_BF16) return vec ? run_forward<bf16, true>(p, mode, st) : run_forward<bf16, false>(p, mode, st);
   return vec ? run_forward<float, true>(p, mode, st) : run_forward<float, false>(p, mode, st);

@@ -161,6 +161,8 @@ __device__ __forceinline__ Gates gates2(float2 r, float2 g, float2 rate2 /* rate
 // gate and β's square root, and a is a polynomial too, so a position takes four
 // special-function operations instead of six, and no choice by cases.  Both
 // polynomials are fitted on [−0.5, 0] for the least relative error (under 2^-24).
+// 8 x 4096 x 4096, bf16: scan 185 us, gradient 396; with any decay (above) 219
+// and 449.  A block decides by its channels' lam.
 constexpr float NEAR_RATE2 = -0.5f;
 __device__ __forceinline__ float2 near_decay(float2 l2) {   // 2^l2
   float2 c = __ffma2_rn(l2, two(0.00115445221f), two(0.0095412815f));
