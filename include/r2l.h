@@ -382,7 +382,8 @@ R2L_API r2l_status r2l_sidecar_forward_train(const void *hidden, void *out, cons
  * r2l_reverse_scan does, or the other way with R2L_FLAG_FORWARD_SCAN.  A state
  * may enter (h0) and leave (h_last), so a sequence can be scanned in pieces, a
  * piece of one position being one step of decoding.  r = −∞ closes the
- * recurrence gate: a_k = 1, and the position leaves the state as it was.
+ * recurrence gate: a_k = 1, and the position, its x being finite, leaves the
+ * state as it was (0 times an infinity or a NaN is NaN here as elsewhere).
  * State, gates and sums are fp32 for both dtypes.
  *
  * r2l_dims: d_inner is the number of channels E (any positive number), dtype
@@ -421,8 +422,9 @@ typedef struct {
  * fp32 [B, E], the state that leaves the scan, or NULL; it may be in->h0.
  * status: device word that receives the R2L_DEVFLAG_* bits of this call (what
  * r2l_get_device_status reads), or NULL.  No workspace is needed, and nothing
- * is enqueued on an error.  The result does not depend on the other sequences
- * of the batch or on B; it is bitwise reproducible for given B, L and E.     */
+ * is enqueued on an error.  A sequence's result does not depend on the other
+ * sequences' values; it is bitwise reproducible for given B, L and E, which
+ * choose how the work is cut.                                                */
 R2L_API r2l_status r2l_gated_scan(const r2l_gated_in *in, void *y, int ldy, float *h_last, const r2l_dims *dims,
                                   int B, int L, const int32_t *lengths, uint32_t *status, void *stream);
 
@@ -482,7 +484,7 @@ R2L_API r2l_status r2l_gated_scan_backward(const r2l_gated_in *in, const void *d
 /* Packs x (dtype, [B·L, ldx], its first `cols` columns) into q ([B·L, ldq]
  * bytes, e4m3) and scales ([B·L, ⌈cols / R2L_ACT8_GROUP⌉] bytes).  lengths as
  * for r2l_sidecar_forward (NULL: all rows); rows i ≥ len_b are neither read
- * nor written.                                                               */
+ * nor written.  The output may not overlap the input, here or in unpacking.  */
 R2L_API r2l_status r2l_act8_pack(const void *x, int ldx, r2l_dtype dtype, int B, int L, int cols,
                                  const int32_t *lengths, uint8_t *q, int ldq, uint8_t *scales, void *stream);
 

@@ -236,6 +236,7 @@ r2l_status check(const void* rows, int ld, r2l_dtype dtype, int B, int L, int co
   if (B <= 0 || L <= 0 || cols <= 0 || (dtype != R2L_BF16 && dtype != R2L_FP32) || !scales) return R2L_ERR_INVALID_ARG;
   R2L_TRY(check_rows(rows, ld, cols, elem_bytes(dtype)));
   R2L_TRY(check_rows(q, ldq, cols, 1));
+  if (rows == q || rows == scales || q == scales) return R2L_ERR_INVALID_ARG;
   if (!aligned(lengths, 4)) return R2L_ERR_ALIGNMENT;
   return fits(B, L, cols) && grid_of(B, L, cols) <= 2147483647LL ? R2L_OK : R2L_ERR_UNSUPPORTED;
 }

@@ -134,10 +134,12 @@ def test_backward_refusals(lib):
 
 
 def test_act8_refusals(lib):
-    def pack(x=FAKE, ldx=100, dtype=0, B=2, L=10, cols=100, lengths=None, q=FAKE, ldq=100, scales=FAKE):
+    Q, SC = FAKE + 4096, FAKE + 8192
+
+    def pack(x=FAKE, ldx=100, dtype=0, B=2, L=10, cols=100, lengths=None, q=Q, ldq=100, scales=SC):
         return lib.r2l_act8_pack(x, ldx, dtype, B, L, cols, lengths, q, ldq, scales, None)
 
-    def unpack(q=FAKE, ldq=100, scales=FAKE, dtype=0, B=2, L=10, cols=100, lengths=None, out=FAKE, ldo=100):
+    def unpack(q=Q, ldq=100, scales=SC, dtype=0, B=2, L=10, cols=100, lengths=None, out=FAKE, ldo=100):
         return lib.r2l_act8_unpack(q, ldq, scales, dtype, B, L, cols, lengths, out, ldo, None)
 
     for f, rows, ld in ((pack, "x", "ldx"), (unpack, "out", "ldo")):
@@ -151,6 +153,8 @@ def test_act8_refusals(lib):
         assert f(**{rows: FAKE + 1}) == 3
         assert f(dtype=1, **{rows: FAKE + 2}) == 3
         assert f(lengths=FAKE + 2) == 3
+        assert f(q=FAKE) == 1 and f(scales=FAKE) == 1 and f(scales=Q) == 1      # one buffer for two
+        assert f(L=2 ** 30 + 1) == 2
 
 
 def test_binding_takes_device_tensors_only(lib):

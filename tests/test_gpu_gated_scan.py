@@ -120,6 +120,9 @@ SHAPES = [
     (3, 63, 96, [63, 1, 0]), (2, 64, 128, None), (2, 65, 63, [64, 65]), (4, 130, 72, [0, 127, 128, 129]),
     (2, 257, 200, [200, 257]), (1, 777, 515, None), (9, 33, 24, [33, 32, 31, 17, 16, 15, 2, 1, 0]), (300, 5, 8, None),
     (2, 1300, 64, None), (1, 3000, 192, None),
+    # sequences of all lengths shared by a cluster, blocks of 8 warps by themselves, and threads that walk
+    (3, 1500, 64, [0, 1500, 700]), (4, 600, 40, [600, 513, 1, 64]), (3, 1100, 2100, [1100, 0, 1025]),
+    (640, 12, 6, [b % 13 for b in range(640)]),
 ]
 
 
@@ -366,6 +369,31 @@ def test_infinite_gates_in_8_bits(dtype, fast):
     for k, v in out.items():
         assert bool(torch.isfinite(v.float()).all()), k
     check_backward(d, out, B, L, False, ("x8", "r8", "g8"))
+
+
+def test_optional_results_left_out():
+    """The C entry points without h_last, status and dh0 (the binding always asks for them)."""
+    B, L, E, dtype = 2, 70, 96, BF16
+    for L in (1, 70, 1300):
+        d = make(B, L, E, dtype, seed=23)
+        c = dev(d)
+        lib, dims = bd.load(), bd.gated_dims(E, dtype)
+        y0, _, ck0, out0 = train(d, c, B, L, E, dtype, False, False)
+        gi = bd.GatedIn(*(c[k].data_ptr() for k in ("x", "r", "g")), E, E, E, c["lam"].data_ptr(), c["h0"].data_ptr())
+        st = torch.cuda.current_stream().cuda_stream
+        y = torch.empty_like(y0)
+        assert lib.r2l_gated_scan(gi, y.data_ptr(), E, None, dims, B, L, None, None, st) == 0
+        check_forward(d, y, bd.gated_scan(c["x"], c["r"], c["g"], c["lam"], dims, B, L, h0=c["h0"])[1], B, L, False)
+        ck = torch.empty_like(ck0)
+        assert lib.r2l_gated_scan_train(gi, y.data_ptr(), E, None, dims, B, L, None, ck.data_ptr(), ck.numel(), None, st) == 0
+        assert torch.equal(y, y0)
+        dx, dr, dg = (torch.empty_like(y0) for _ in range(3))
+        dlam = torch.empty(E, device="cuda")
+        ws = torch.empty(bd.gated_scan_backward_workspace_size(dims, B, L), dtype=torch.uint8, device="cuda")
+        gr = bd.GatedGrads(dx.data_ptr(), dr.data_ptr(), dg.data_ptr(), E, E, E, dlam.data_ptr(), None)
+        assert lib.r2l_gated_scan_backward(gi, c["dy"].data_ptr(), E, c["dh_last"].data_ptr(), gr, dims, B, L, None,
+                                           ck.data_ptr(), ck.numel(), ws.data_ptr(), ws.numel(), st) == 0
+        assert all(torch.equal(a, out0[k]) for a, k in ((dx, "dx"), (dr, "dr"), (dg, "dg"), (dlam, "dlam")))
 
 
 def test_many_sequences():
