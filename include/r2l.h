@@ -394,10 +394,13 @@ R2L_API r2l_status r2l_sidecar_forward_train(const void *hidden, void *out, cons
  * can be columns of a wider array; row b·L + i is position i of sequence b.
  * Pointers need the alignment of their element type only; a call whose arrays
  * of rows all start on 16-byte boundaries with strides that are multiples of
- * 16 bytes runs faster.  No output may overlap an input, except h_last = h0
- * and dh0 = dh_last.  lengths as for r2l_sidecar_forward (clamped to [0, L];
- * a sequence of length 0 passes its state through).  E and L up to 2^30 and
- * B · L · E up to 2^50; more returns R2L_ERR_UNSUPPORTED.
+ * 16 bytes runs faster.  Between the start of an array's first row and the
+ * end of its last one, up to 15 bytes beside a row's E columns may be read
+ * (nothing depends on them); they are never written.  No output may overlap an
+ * input, except h_last = h0 and dh0 = dh_last.  lengths as for
+ * r2l_sidecar_forward (clamped to [0, L]; a sequence of length 0 passes its
+ * state through).  E and L up to 2^30 and B · L · E up to 2^50; more returns
+ * R2L_ERR_UNSUPPORTED.
  * ------------------------------------------------------------------------- */
 #define R2L_GATED_RATE 8.0f
 #define R2L_GATED_TILE 64   /* positions between two states of a checkpoint */

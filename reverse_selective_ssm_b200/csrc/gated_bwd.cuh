@@ -24,11 +24,36 @@ namespace gated {
 constexpr float TINY = 1.17549435e-38f;
 constexpr int BL = 16;                     // lanes of a row
 
+// One element to shared memory, or 0 where it does not exist (`from` is valid all the same).
+__device__ __forceinline__ void copy_element(float* to, const float* from, bool exists) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_addr(to)), "l"(from), "r"(exists ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_element(bf16* to, const bf16* from, bool exists) {
+  *to = exists ? *from : from_f32<bf16>(0.0f);
+}
+
+// Rows that start anywhere, of which `cols` channels exist (the others are 0),
+// element by element: whole 16-byte pieces (copy_any) cost registers that the
+// gradient has not (5 ragged x 777 x 515, fp32: 27 us, and 44 with pieces);
+// `first` is position 0 at the block's first channel.
+template <typename T, typename LAY>
+__device__ __forceinline__ void copy_elements(T* dst, const T* first, int step, int k, int n, int cols, int wl) {
+  static_assert(LAY::CHANNELS % 32 == 0, "a lane copies a channel");
+#pragma unroll
+  for (int c = 0; c < LAY::CHANNELS; c += 32) {
+    const bool exists = c + wl < cols;
+    const T* const from = first + (exists ? c + wl : 0);
+#pragma unroll 8
+    for (int row = 0; row < LAY::WARP_ROWS; ++row)
+      copy_element(dst + LAY::at(row) + c + wl, from + (long long)min(k + row, n - 1) * step, exists);
+  }
+}
+
 template <typename T, bool ACT8, int WARPS>
 struct BwdSmem {
   typedef typename std::conditional<ACT8, uint8_t, T>::type Q;
-  Q in[2][3][WARPS * Layout<Q, BL, ROWS>::WARP_STRIDE];
-  T dy[2][WARPS * Layout<T, BL, ROWS>::WARP_STRIDE];
+  Q in[2][3][WARPS * Layout<Q, BL, ROWS, false>::WARP_STRIDE];
+  T dy[2][WARPS * Layout<T, BL, ROWS, false>::WARP_STRIDE];
   uint8_t scales[2][WARPS][3][2 * ROWS];
   float states[2][WARPS][2 * BL];          // each warp's copy of its 64 positions' first state
   float4 maps[2][WARPS][BL];               // D leaves = A · D enters + B
@@ -52,8 +77,8 @@ __global__ void __launch_bounds__(WARPS * 32, (sizeof(T) == 2 || WARPS == 8 ? 16
     gated_bwd_kernel(const BwdArgs p, const uint32_t blocks) {
   typedef BwdSmem<T, ACT8, WARPS> Smem;
   typedef typename Smem::Q Q;
-  typedef Layout<Q, BL, ROWS> LayQ;
-  typedef Layout<T, BL, ROWS> Lay;
+  typedef Layout<Q, BL, ROWS, false> LayQ;
+  typedef Layout<T, BL, ROWS, false> Lay;
   constexpr int SPAN = WARPS * Lay::WARP_ROWS, TILE_WARPS = TILE / Lay::WARP_ROWS;
   extern __shared__ __align__(16) unsigned char smem_raw[];
   Smem& sm = *reinterpret_cast<Smem*>(smem_raw);

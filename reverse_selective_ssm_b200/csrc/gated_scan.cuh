@@ -229,31 +229,26 @@ __device__ __forceinline__ void copies_wait() {
 // Threads of a warp and their rows.  LANES lanes hold a row of 2 · LANES
 // channels, two each, so a warp has 32 / LANES groups of ROWS consecutive rows;
 // in shared memory a group is followed by 64 bytes of nothing, which puts two
-// groups that are read together into different banks.
-template <typename T, int LANES, int ROWS>
+// groups that are read together into different banks.  ANY: rows start
+// anywhere in memory; a row in shared memory then starts as far from a
+// 16-byte boundary as in memory, and has 16 bytes more.
+template <typename T, int LANES, int ROWS, bool ANY>
 struct Layout {
   static constexpr int CHANNELS = 2 * LANES;
   static constexpr int GROUPS = 32 / LANES;                  // of a warp
-  static constexpr int GROUP_STRIDE = ROWS * CHANNELS + (GROUPS > 1 ? 64 / (int)sizeof(T) : 0);   // elements
-  static constexpr int WARP_STRIDE = GROUPS * GROUP_STRIDE;
   static constexpr int PER = 16 / (int)sizeof(T);            // elements of a copy
+  static constexpr int ROW = CHANNELS + (ANY ? PER : 0);     // elements from row to row
+  static constexpr int GROUP_STRIDE = ROWS * ROW + (GROUPS > 1 && !ANY ? 64 / (int)sizeof(T) : 0);
+  static constexpr int WARP_STRIDE = GROUPS * GROUP_STRIDE;
   static constexpr int CHUNKS = CHANNELS / PER;              // copies of a row
   static constexpr int AT_ONCE = 32 / CHUNKS;                // rows that a warp's lanes copy at once
   static constexpr int WARP_ROWS = ROWS * GROUPS;
-  static_assert(ROWS % AT_ONCE == 0 || AT_ONCE == WARP_ROWS, "at(i + j) = at(i) + at(j) for the rows of a copy");
-  static __device__ __forceinline__ int at(int row) { return row / ROWS * GROUP_STRIDE + row % ROWS * CHANNELS; }
+  static_assert(ANY || ROWS % AT_ONCE == 0 || AT_ONCE == WARP_ROWS, "at(i + j) = at(i) + at(j) for the rows of a copy");
+  static __device__ __forceinline__ int at(int row) { return row / ROWS * GROUP_STRIDE + row % ROWS * ROW; }
   // This lane's chunk of the first rows that are copied at once.
   static __device__ __forceinline__ int chunk(int wl) { return at(wl / CHUNKS) + channel(wl); }
   static __device__ __forceinline__ int channel(int wl) { return wl % CHUNKS * PER; }
 };
-
-// One element to shared memory, or 0 where it does not exist (`from` is valid all the same).
-__device__ __forceinline__ void copy_element(float* to, const float* from, bool exists) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_addr(to)), "l"(from), "r"(exists ? 4 : 0) : "memory");
-}
-__device__ __forceinline__ void copy_element(bf16* to, const bf16* from, bool exists) {
-  *to = exists ? *from : from_f32<bf16>(0.0f);
-}
 
 // The rows of a warp from position k on, on their way to dst in shared memory.
 // A warp copies only the rows that it reads itself, so a copy needs no barrier
@@ -270,18 +265,45 @@ __device__ __forceinline__ void copy_rows(uint32_t dst, const T* first, int step
   for (int i = 0; i < LAY::WARP_ROWS; i += LAY::AT_ONCE)
     copy16(dst + LAY::at(i) * (int)sizeof(T), first + (long long)min(k + i, n - 1) * step, exists);
 }
-// copy_elements: any rows, of which `cols` channels exist (the others are 0);
-// `first` is position 0 at the block's first channel.
+
+// Elements from the 16-byte boundary before position k (of a sequence whose
+// position 0 is at `first`) to it.
+template <typename T>
+__device__ __forceinline__ int offset_of(const T* first, int step, int k) {
+  return (int)((uint32_t)((uintptr_t)first / sizeof(T)) + (uint32_t)k * (uint32_t)step) & (16 / (int)sizeof(T) - 1);
+}
+// Positions of a sequence whose row has nothing of the array before it, or
+// nothing behind it (−1: none).
+struct Edges {
+  int head, tail;
+};
+__device__ __forceinline__ Edges array_edges(int b, int B, int n, int L, bool forward) {
+  return {b == 0 && n > 0 ? (forward ? 0 : n - 1) : -1, b == B - 1 && n == L ? (forward ? L - 1 : 0) : -1};
+}
+// copy_any: rows that start anywhere.  The 16-byte pieces of memory that hold
+// a row's channels are copied whole, with what they hold of the rows beside
+// it, which no result uses; the array's first and last row, whose pieces may
+// reach outside it, go element by element, as do rows shorter than a piece.
+// `first` is position 0 at the block's first channel, of which `cols` exist.
+// All rows element by element: 61 ragged x 512 x 1037, fp32, 100 us, here 70;
+// 8 x 2000 x 1037, bf16, 86 and 53.  The 8-bit forward of 5 ragged x
+// 777 x 515, fp32, loses by it, 27 us and 30.
 template <typename T, typename LAY>
-__device__ __forceinline__ void copy_elements(T* dst, const T* first, int step, int k, int n, int cols, int wl) {
-  static_assert(LAY::CHANNELS % 32 == 0, "a lane copies a channel");
+__device__ __forceinline__ void copy_any(T* dst, const T* first, int step, int k, int n, int cols, const Edges& edges, int wl) {
+  constexpr int PIECES = LAY::CHUNKS + 1;
 #pragma unroll
-  for (int c = 0; c < LAY::CHANNELS; c += 32) {
-    const bool exists = c + wl < cols;
-    const T* const from = first + (exists ? c + wl : 0);
-#pragma unroll 8
-    for (int row = 0; row < LAY::WARP_ROWS; ++row)
-      copy_element(dst + LAY::at(row) + c + wl, from + (long long)min(k + row, n - 1) * step, exists);
+  for (int i = 0; i < (LAY::WARP_ROWS * PIECES + 31) / 32; ++i) {
+    const int row = (i * 32 + wl) / PIECES, piece = (i * 32 + wl) % PIECES, pos = min(k + row, n - 1);
+    const int from = piece * LAY::PER - offset_of(first, step, pos);      // channel at the piece's start
+    if (row >= LAY::WARP_ROWS || from >= cols) continue;
+    T* const to = dst + LAY::at(row) + piece * LAY::PER;
+    const T* const src = first + (long long)pos * step + from;
+    if (pos != edges.head && pos != edges.tail && abs(step) >= LAY::PER) {
+      copy16(smem_addr(to), src);
+    } else {
+      for (int c = 0; c < LAY::PER; ++c)
+        if (from + c >= 0 && from + c < cols) to[c] = src[c];
+    }
   }
 }
 // v in all channels of the rows from `rows` on, of a warp that has no more.
@@ -289,7 +311,7 @@ template <typename T, typename LAY>
 __device__ __forceinline__ void fill_rows(T* dst, int wl, int rows, float v) {
 #pragma unroll 1
   for (int row = rows; row < LAY::WARP_ROWS; ++row)
-    for (int c = wl; c < LAY::CHANNELS; c += 32) dst[LAY::at(row) + c] = from_f32<T>(v);
+    for (int c = wl; c < LAY::ROW; c += 32) dst[LAY::at(row) + c] = from_f32<T>(v);
 }
 
 __device__ __forceinline__ float2 lane_pair(const float* row, int lane) {
@@ -298,6 +320,12 @@ __device__ __forceinline__ float2 lane_pair(const float* row, int lane) {
 __device__ __forceinline__ float2 lane_pair(const bf16* row, int lane) {
   const uint32_t v = reinterpret_cast<const uint32_t*>(row)[lane];
   return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+}
+
+// A lane's pair of a row that starts anywhere, 0 for channels past the last.
+template <typename T>
+__device__ __forceinline__ float2 any_pair(const T* row, int lane, int cols) {
+  return make_float2(2 * lane < cols ? to_f32(row[2 * lane]) : 0.0f, 2 * lane + 1 < cols ? to_f32(row[2 * lane + 1]) : 0.0f);
 }
 
 // Row j from p, a step of `step` elements (32 bits: one multiply-add forms the address).
@@ -311,14 +339,21 @@ __device__ __forceinline__ void store_if(uint16_t* at, int j, int rows, uint16_t
                "h"(v)
                : "memory");
 }
-// The larger magnitude of a lane's two channels, as the bits of a float (from 0x7f800000 on: not finite).
-__device__ __forceinline__ uint32_t lane_abs_max(const float* row, int lane) {
-  const float2 v = lane_pair(row, lane);
+// The larger magnitude of two channels, as the bits of a float (from 0x7f800000 on: not finite).
+__device__ __forceinline__ uint32_t abs_max(float2 v) {
   return max(__float_as_uint(v.x) & 0x7fffffffu, __float_as_uint(v.y) & 0x7fffffffu);
 }
+// The same of a lane's pair of a row.
+__device__ __forceinline__ uint32_t lane_abs_max(const float* row, int lane) { return abs_max(lane_pair(row, lane)); }
 __device__ __forceinline__ uint32_t lane_abs_max(const bf16* row, int lane) {
   const uint32_t w = reinterpret_cast<const uint32_t*>(row)[lane] & 0x7fff7fffu;
   return max(w, w << 16) & 0xffff0000u;
+}
+
+__device__ __forceinline__ void store_if(float* at, int j, int rows, float v) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.lt.s32 p, %0, %1;\n\t@p st.global.f32 [%2], %3;\n\t}" ::"r"(j), "r"(rows), "l"(at),
+               "f"(v)
+               : "memory");
 }
 
 // What an 8-bit checkpoint holds of values that need not be finite: a gate at
@@ -329,12 +364,6 @@ __device__ __forceinline__ float storable(float v, bool gate) {
 }
 __device__ __forceinline__ float2 storable(float2 v, bool gate) {
   return make_float2(storable(v.x, gate), storable(v.y, gate));
-}
-
-__device__ __forceinline__ void store_if(float* at, int j, int rows, float v) {
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.lt.s32 p, %0, %1;\n\t@p st.global.f32 [%2], %3;\n\t}" ::"r"(j), "r"(rows), "l"(at),
-               "f"(v)
-               : "memory");
 }
 
 // A lane's two channels at `at`, where j < rows (as a predicate, not a branch).
@@ -457,23 +486,23 @@ __device__ __forceinline__ float2 other_half(float2 v) {
 constexpr int ROWS = 8;      // consecutive rows of a thread
 
 // In shared memory, behind it the maps of the cluster's blocks, [2][blocks][LANES].
-template <typename T, int LANES, int WARPS>
+template <typename T, bool VEC, int LANES, int WARPS>
 struct FwdSmem {
-  T in[2][3][WARPS * Layout<T, LANES, ROWS>::WARP_STRIDE];
+  T in[2][3][WARPS * Layout<T, LANES, ROWS, !VEC>::WARP_STRIDE];
   float4 maps[2][WARPS][LANES];
   float2 carry[WARPS][LANES];
 };
-template <typename T, int LANES, int WARPS>
+template <typename T, bool VEC, int LANES, int WARPS>
 constexpr size_t fwd_smem_bytes(uint32_t blocks) {
-  return sizeof(FwdSmem<T, LANES, WARPS>) + (blocks > 1 ? 2 * sizeof(float4) * LANES * blocks : 0);
+  return sizeof(FwdSmem<T, VEC, LANES, WARPS>) + (blocks > 1 ? 2 * sizeof(float4) * LANES * blocks : 0);
 }
 
 // MODE 0: the recurrence; 1: also the states of a checkpoint; 2: and its 8 bits.
 template <typename T, bool VEC, int MODE, int LANES, int WARPS>
 __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
     gated_scan_kernel(const FwdArgs p, const uint32_t blocks) {
-  typedef Layout<T, LANES, ROWS> Lay;
-  typedef FwdSmem<T, LANES, WARPS> Smem;
+  typedef Layout<T, LANES, ROWS, !VEC> Lay;
+  typedef FwdSmem<T, VEC, LANES, WARPS> Smem;
   static_assert(MODE < 2 || LANES == 32, "the channels of a scale are a row of the warp");
   constexpr int SPAN = WARPS * Lay::WARP_ROWS;      // rows of the block's tile
   extern __shared__ __align__(16) unsigned char smem_raw[];
@@ -504,6 +533,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
   T* const rows0 = sm.in[0][0] + warp * Lay::WARP_STRIDE;
 
   const uint32_t chunk0 = smem_addr(rows0 + Lay::chunk(wl));
+  const Edges edges = array_edges(b, p.B, n, p.L, p.forward);
   auto load = [&](int buf, int k) {
     if (k < n) {
       if constexpr (VEC) {
@@ -513,9 +543,9 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
         copy_rows<T, Lay>(to + 2 * ARRAY * (int)sizeof(T), g0, g_step, k, n, wl, exists);
       } else {
         T* const to = rows0 + buf * 3 * ARRAY;
-        copy_elements<T, Lay>(to, x0, x_step, k, n, cols, wl);
-        copy_elements<T, Lay>(to + ARRAY, r0, r_step, k, n, cols, wl);
-        copy_elements<T, Lay>(to + 2 * ARRAY, g0, g_step, k, n, cols, wl);
+        copy_any<T, Lay>(to, x0, x_step, k, n, cols, edges, wl);
+        copy_any<T, Lay>(to + ARRAY, r0, r_step, k, n, cols, edges, wl);
+        copy_any<T, Lay>(to + 2 * ARRAY, g0, g_step, k, n, cols, edges, wl);
       }
     }
     copies_commit();
@@ -538,6 +568,16 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
       const T* const in = rows0 + buf * 3 * ARRAY + half * Lay::GROUP_STRIDE;
       copies_wait<1>();
       __syncwarp();
+      // rows that start anywhere: where this group's first ones do (rows past the end are filled from any start)
+      const int first = k + half * ROWS, x_offset = VEC ? 0 : offset_of(x0, x_step, first),
+                r_offset = VEC ? 0 : offset_of(r0, r_step, first), g_offset = VEC ? 0 : offset_of(g0, g_step, first);
+      auto value = [&](int i, int j) {      // x, r or g of row j of this group
+        const T* const at = in + i * ARRAY + j * Lay::ROW;
+        if constexpr (VEC) return lane_pair(at, lane);
+        const uint32_t offset = (i == 0 ? x_offset : i == 1 ? r_offset : g_offset) +
+                                (uint32_t)j * (uint32_t)(i == 0 ? x_step : i == 1 ? r_step : g_step);
+        return any_pair(at + (offset & (Lay::PER - 1)), lane, cols);
+      };
       float2 P[ROWS], H[ROWS];     // row j's state is P[j] · (state that enters the group) + H[j]
       float2 a = two(1.0f), h = two(0.0f);
       if (left > 0) {
@@ -560,14 +600,15 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
           for (int i = 0; i < 3; ++i)
 #pragma unroll
             for (int j = 0; j < ROWS; ++j) {
-              const uint32_t m = __reduce_max_sync(0xffffffffu, lane_abs_max(in + i * ARRAY + j * Lay::CHANNELS, lane));
+              const uint32_t m = __reduce_max_sync(
+                    0xffffffffu, VEC ? lane_abs_max(in + i * ARRAY + j * Lay::ROW, lane) : abs_max(value(i, j)));
               if (lane == i * ROWS + j) top = m;
             }
           const bool odd = __any_sync(0xffffffffu, top >= 0x7f800000u);
           if (odd) {
 #pragma unroll 1
             for (int c = 0; c < 3 * ROWS; ++c) {
-              const float2 v = storable(lane_pair(in + c / ROWS * ARRAY + c % ROWS * Lay::CHANNELS, lane), c >= ROWS);
+              const float2 v = storable(value(c / ROWS, c % ROWS), c >= ROWS);
               const uint32_t m = __reduce_max_sync(0xffffffffu, max(act8::finite_abs_bits(v.x), act8::finite_abs_bits(v.y)));
               if (lane == c) top = m;
             }
@@ -581,7 +622,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
             uint16_t* const q = reinterpret_cast<uint16_t*>(p.ck.q[i] + (strip * p.L + k) * STRIP) + lane;
 #pragma unroll
             for (int j = 0; j < ROWS; ++j) {
-              float2 v = lane_pair(in + i * ARRAY + j * Lay::CHANNELS, lane);
+              float2 v = value(i, j);
               if (odd) v = storable(v, i > 0);
               v = __fmul2_rn(v, two(__shfl_sync(0xffffffffu, down, i * ROWS + j)));
               store_if(q + j * (STRIP / 2), j, left, act8::to_e4m3x2(v.x, v.y));
@@ -591,8 +632,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
 #pragma unroll
         for (int j = 0; j < ROWS; ++j) {
           float2 aj, bj;
-          coefficients<NEAR>(lane_pair(in + j * Lay::CHANNELS, lane), lane_pair(in + ARRAY + j * Lay::CHANNELS, lane),
-                             lane_pair(in + 2 * ARRAY + j * Lay::CHANNELS, lane), rate2, scale, aj, bj);
+          coefficients<NEAR>(value(0, j), value(1, j), value(2, j), rate2, scale, aj, bj);
           a = j == 0 ? aj : __fmul2_rn(a, aj);
           h = j == 0 ? bj : __ffma2_rn(aj, h, bj);
           P[j] = a;

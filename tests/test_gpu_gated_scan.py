@@ -281,6 +281,34 @@ def test_columns_of_wider_arrays(dtype):
         assert torch.all(outs[:, 4 * pad:] == 7.0)
 
 
+@pytest.mark.parametrize("E", [1, 3, 5, 31, 63, 129])
+@pytest.mark.parametrize("forward", [False, True], ids=["r2l", "l2r"])
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
+def test_rows_that_start_anywhere_among_nan(dtype, forward, E):
+    """Each array in a buffer of NaN, with its own start and its own distance from row to row, some without a gap, in
+    both forms of the training forward."""
+    B, L = 3, 150
+    d = make(B, L, E, dtype, seed=31 + E, lens=[150, 0, 131])
+    poison(d, L)
+    c = dev(d)
+
+    def among_nan(t, start, gap):
+        buf = torch.full((start + B * L * (E + gap) + 9,), float("nan"), dtype=dtype, device="cuda")
+        at = buf.as_strided((B * L, E), (E + gap, 1), start)
+        at.copy_(t)
+        return at
+
+    dims, lens = bd.gated_dims(E, dtype, flags=flags_of(forward)), lengths_tensor(d, L)
+    for start, gap in ((1, 0), (7, 2), (4, 5)):
+        x, r, g = (among_nan(c[k], start + 3 * j, gap + j) for j, k in enumerate(("x", "r", "g")))
+        y, h = bd.gated_scan(x, r, g, c["lam"], dims, B, L, lengths=lens, h0=c["h0"])
+        check_forward(d, y, h, B, L, forward)
+        for act8 in (False, True):
+            dims_t = bd.gated_dims(E, dtype, flags=flags_of(forward, act8))
+            y_t, h_t, _ = bd.gated_scan_train(x, r, g, c["lam"], dims_t, B, L, lengths=lens, h0=c["h0"])
+            check_forward(d, y_t, h_t, B, L, forward)
+
+
 @pytest.mark.parametrize("forward", [False, True], ids=["r2l", "l2r"])
 def test_pieces_and_steps_give_the_whole(forward):
     """A sequence in pieces, the state handed on, down to single tokens: decoding after a prefill."""
