@@ -79,6 +79,7 @@ struct BwdArgs {
 // ---------------------------------------------------------------- arithmetic
 
 constexpr float LOG2E = 1.4426950408889634f, LN2 = 0.6931471805599453f;
+constexpr float LOG2E_REST = (float)(1.4426950408889634 - (double)LOG2E);     // log2 e − LOG2E
 
 __device__ __forceinline__ float ex2(float x) {
   float y;
@@ -109,7 +110,7 @@ __device__ __forceinline__ float2 two(float v) { return make_float2(v, v); }
 // of log1pf(expf()), which were most of a decoding step.
 __device__ __forceinline__ float decay_rate(float lam) {
   const float v = -fabsf(lam), t = v * LOG2E;
-  const float rest = fmaf(v, LOG2E, -t) + v * 1.925963033500e-8f;     // of v · log2 e
+  const float rest = fmaf(v, LOG2E, -t) + v * LOG2E_REST;     // of v · log2 e
   const float e0 = ex2(t), e = fmaf(e0, rest * LN2, e0);
   const float z = e * rcp(2.0f + e), q = z * z;
   float c = fmaf(q, 1.0f / 15.0f, 1.0f / 13.0f);
