@@ -384,7 +384,9 @@ R2L_API r2l_status r2l_sidecar_forward_train(const void *hidden, void *out, cons
  * piece of one position being one step of decoding.  r = −∞ closes the
  * recurrence gate: a_k = 1, and the position, its x being finite, leaves the
  * state as it was (0 times an infinity or a NaN is NaN here as elsewhere).
- * State, gates and sums are fp32 for both dtypes.
+ * lam = −∞ keeps the state throughout, lam = +∞ forgets it at any gate that is
+ * not closed (softplus(lam) is held to 2^124, and a σ(r) below 2^-126 may count
+ * as closed).  State, gates and sums are fp32 for both dtypes.
  *
  * r2l_dims: d_inner is the number of channels E (any positive number), dtype
  * the type of the [B·L, ·] arrays, flags R2L_FLAG_FORWARD_SCAN and

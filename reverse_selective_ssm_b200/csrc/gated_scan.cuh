@@ -106,10 +106,15 @@ __device__ __forceinline__ float2 two(float v) { return make_float2(v, v); }
 // −R2L_GATED_RATE · softplus(lam), log a at an open gate.  With e = e^−|lam|
 // (the rounding of the exponent's product made up for) and z = e / (2 + e),
 // log(1 + e) = 2 atanh z = 2z (1 + z²/3 + z⁴/5 + …), z ≤ 1/3: seven terms leave
-// a relative error of a few 2^-24 for every lam, in a fifth of the instructions
-// of log1pf(expf()), which were most of a decoding step.
+// a relative error of a few 2^-24, in a fifth of the instructions of
+// log1pf(expf()), which were most of a decoding step.  An e below 2^-126
+// (lam < −87) counts as 0, a decay that fp32 cannot tell from 1; |lam| is held to
+// 128 there, so that ±∞ makes no ∞ − ∞.  softplus(lam) is held to 2^124: log2 a
+// at an open gate is then finite, and 0 times it, a closed gate, is 0 for every
+// lam.  A NaN passes both limits.
+constexpr float SOFTPLUS_MAX = 0x1p124f;
 __device__ __forceinline__ float decay_rate(float lam) {
-  const float v = -fabsf(lam), t = v * LOG2E;
+  const float w = -fabsf(lam), v = w < -128.0f ? -128.0f : w, t = v * LOG2E;
   const float rest = fmaf(v, LOG2E, -t) + v * LOG2E_REST;     // of v · log2 e
   const float e0 = ex2(t), e = fmaf(e0, rest * LN2, e0);
   const float z = e * rcp(2.0f + e), q = z * z;
@@ -120,7 +125,7 @@ __device__ __forceinline__ float decay_rate(float lam) {
   c = fmaf(c, q, 1.0f / 5.0f);
   c = fmaf(c, q, 1.0f / 3.0f);
   c = fmaf(c, q, 1.0f);
-  return -R2L_GATED_RATE * fmaf(2.0f * z, c, fmaxf(lam, 0.0f));
+  return -R2L_GATED_RATE * fmaf(2.0f * z, c, fminf(fmaxf(lam, 0.0f), SOFTPLUS_MAX));
 }
 
 // 1 + 2^(−v log2 e), whose reciprocal is σ(v): ∞ at −∞ and 1 at +∞.

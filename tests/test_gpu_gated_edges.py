@@ -1,0 +1,63 @@
+"""Calls at the edges of what the gated scan and the 8-bit checkpoints accept: parameters without bounds, gates far out
+and values near a type's largest, on the GPU against the float64 oracle (tolerances as in test_gpu_gated_scan.py)."""
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+from reverse_selective_ssm_b200 import binding as bd
+from reverse_selective_ssm_b200 import synthetic as S
+
+from .test_gpu_gated_scan import check_backward, check_forward, dev, flags_of, lengths_tensor, make, train
+
+pytestmark = pytest.mark.gpu
+
+BF16, FP32 = torch.bfloat16, torch.float32
+INF = float("inf")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    bd.load()
+
+
+@pytest.mark.parametrize("L", [1, 3, 200, 1300])
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
+def test_decay_parameters_without_bounds(dtype, L):
+    """lam at ±inf and out to fp32's largest: a channel that never forgets keeps its state bit for bit, one that forgets
+    at once holds its input alone, and a closed gate keeps the state even there.  64 channels hold slow ones only, 64
+    both kinds.  The oracle has the limits: at lam = -700 the decay is 1 to the last digit, at 1e30 it is 0."""
+    B, E = 2, 128
+    d = make(B, L, E, dtype, seed=40 + L)
+    slow, fast = [-INF, torch.finfo(FP32).min, -3e38, -2e38, -200.0], [INF, torch.finfo(FP32).max, 3e38, 2e38, 1e30]
+    d["lam"][:5] = d["lam"][64:69] = torch.tensor(slow)
+    d["lam"][70:75] = torch.tensor(fast)
+    d["lam"][75] = INF
+    d["r"][:, 75] = d["r"][:, 3] = -INF
+    c = dev(d)
+    for forward in (False, True):
+        dims = bd.gated_dims(E, dtype, flags_of(forward))
+        y, h, _, out = train(d, c, B, L, E, dtype, forward, False)
+        y2, h2 = bd.gated_scan(c["x"], c["r"], c["g"], c["lam"], dims, B, L, h0=c["h0"])
+        for k in [*range(5), *range(64, 69), 75]:
+            assert torch.equal(h[:, k], c["h0"][:, k]) and torch.equal(h2[:, k], c["h0"][:, k]), k
+        want = dict(d, lam=d["lam"].double().clamp(-700, 1e30))
+        check_forward(want, y, h, B, L, forward)
+        check_forward(want, y2, h2, B, L, forward)
+        for k, v in out.items():
+            assert bool(torch.isfinite(v.float()).all()), k
+        check_backward(want, out, B, L, forward)
+
+
+def test_a_decay_parameter_that_is_nan_shows():
+    B, L, E = 2, 70, 64
+    d = make(B, L, E, FP32, seed=41)
+    d["lam"][7] = float("nan")
+    for n in (1, L):
+        e = {k: v[: B * n] if torch.is_tensor(v) and v.shape[0] == B * L else v for k, v in d.items()}
+        y, h, _, out = train(e, dev(e), B, n, E, FP32, True, False)
+        for t in (y, h, *out.values()):
+            bad = torch.isnan(t).cpu().view(-1, E)
+            assert bool(bad[:, 7].all()) and not bool(bad[:, :7].any()) and not bool(bad[:, 8:].any())
