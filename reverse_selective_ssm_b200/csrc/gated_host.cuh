@@ -51,7 +51,7 @@ inline CkptPlan plan_checkpoint(const r2l_dims* d, int B, int L) {
   k.Lp = (int)align_up(L, 16);
   size_t off = 0;
   k.states = off;
-  off = align_up(off + B * k.tiles * strips * STRIP * sizeof(float), kAlign);
+  off = align_up(off + (size_t)B * k.tiles * strips * STRIP * sizeof(float), kAlign);
   if (d->flags & R2L_FLAG_ACT8)
     for (int i = 0; i < 3; ++i) {
       k.q[i] = off;

@@ -78,6 +78,19 @@ def test_checkpoint_sizes(lib):
     assert big < 0.53 * 3 * 2 * 8 * 4096 * 4096
 
 
+def test_checkpoint_sizes_past_32_bits(lib):
+    """B times the tiles of a sequence passes 2^31, and 2^32, long before B · L · E passes 2^50."""
+    for B, L in ((65536, 2 ** 22), (2 ** 30, 65), (2 ** 31 - 1, 129), (2 ** 20, 2 ** 30)):
+        states = B * -(-L // 64) * 64 * 4
+        assert states <= bd.gated_scan_checkpoint_size(_dims(E=1), B, L) < states + 256
+        got = bd.gated_scan_checkpoint_size(_dims(E=1, flags=bd.R2L_FLAG_ACT8), B, L)
+        least = states + 3 * B * (64 * L + -(-L // 16) * 16)
+        assert least <= got < least + 7 * 256
+        # a buffer of a byte less is refused
+        assert lib.r2l_gated_scan_train(ctypes.byref(_in()), FAKE + 192, 128, None, ctypes.byref(_dims(E=1)), B, L, None, FAKE,
+                                        states - 1, None, None) == 4
+
+
 def test_train_refusals(lib):
     def call(ck=FAKE, nbytes=1 << 40, dims=None, **kw):
         dims = dims or _dims()
