@@ -437,8 +437,9 @@ R2L_API r2l_status r2l_gated_scan(const r2l_gated_in *in, void *y, int ldy, floa
  * input.  Without R2L_FLAG_ACT8 it holds the state that enters every
  * R2L_GATED_TILE-th position of the scan order (fp32, 1/16 byte per position
  * and channel); with it also x, r and g as r2l_act8_pack packs them (3 + 3/64
- * bytes per position and channel), after the same states.  Channels are
- * rounded up to R2L_ACT8_GROUP.                                              */
+ * bytes per position and channel), after the same states; an r or g beyond
+ * ±256, infinite or finite, is kept as ±256, which closes or opens that gate
+ * just the same.  Channels are rounded up to R2L_ACT8_GROUP.                 */
 R2L_API size_t r2l_gated_scan_checkpoint_size(const r2l_dims *dims, int B, int L);
 
 /* r2l_gated_scan for training: also writes `checkpoint`
@@ -463,8 +464,7 @@ R2L_API size_t r2l_gated_scan_backward_workspace_size(const r2l_dims *dims, int 
  * in: x, r, g and lam as given to the forward (h0 is not read: the checkpoint
  * has it).  With R2L_FLAG_ACT8 x, r and g are not read either and may be NULL;
  * the gradient is then the formula at the values that the checkpoint's 8 bits
- * stand for, each tile's states recomputed from its exact first one.  Gates at
- * ±∞ are kept as ±256 there, which closes and opens them just the same.
+ * stand for, each tile's states recomputed from its exact first one.
  * dims, B, L and lengths as given to r2l_gated_scan_train; dims->flags too.
  * Every sum runs in a fixed order: results are bitwise reproducible.
  * workspace ≥ r2l_gated_scan_backward_workspace_size(dims, B, L) bytes,

@@ -61,3 +61,32 @@ def test_a_decay_parameter_that_is_nan_shows():
         for t in (y, h, *out.values()):
             bad = torch.isnan(t).cpu().view(-1, E)
             assert bool(bad[:, 7].all()) and not bool(bad[:, :7].any()) and not bool(bad[:, 8:].any())
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("fast", [False, True], ids=["slow", "fast"])
+@pytest.mark.parametrize("E", [96, 70])
+def test_gates_far_out_in_8_bits(E, fast, dtype):
+    """Masks of -1e9, of the type's lowest value and of -inf, alone and together among the channels of a scale: those
+    gates are closed (or open) in the gradient from 8 bits as they are in the forward, and the other channels' gates
+    come back as those of a row without masks that reaches 256."""
+    B, L = 2, 130
+    d = make(B, L, E, dtype, seed=43)
+    if fast:
+        d["lam"] += 6.0
+    low = torch.finfo(dtype).min
+    d["r"][2::17, ::5], d["r"][5::17, 1::7] = low, -1e9
+    d["r"][5::17, ::9], d["r"][8::17, 3::8] = -INF, -low
+    d["r"][11::17, 4::6], d["r"][11::17, 5::6], d["r"][11::17, 6::6] = -INF, low, 300.0
+    d["r"][14::17, 2::3] = -257.0
+    d["g"][3::13, ::3], d["g"][6::13, 1::4] = low, 1e9
+    d["g"][6::13, ::4], d["g"][9::13, 2::5], d["g"][9::13, 1::5] = -INF, INF, low
+    y, h, _, out = train(d, dev(d), B, L, E, dtype, False, True)
+    check_forward(d, y, h, B, L, False)
+    for k in ("x", "r", "g"):
+        v = S.to_f64(d[k])
+        held = O.act8_values(v if k == "x" else np.clip(v, -256.0, 256.0))
+        d[k + "8"] = torch.from_numpy(held if k == "x" else np.where(np.abs(v) >= 256.0, np.copysign(np.inf, v), held))
+    for k, v in out.items():
+        assert bool(torch.isfinite(v.float()).all()), k
+    check_backward(d, out, B, L, False, ("x8", "r8", "g8"))
