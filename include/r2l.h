@@ -466,7 +466,9 @@ R2L_API size_t r2l_gated_scan_backward_workspace_size(const r2l_dims *dims, int 
  * the gradient is then the formula at the values that the checkpoint's 8 bits
  * stand for, each tile's states recomputed from its exact first one.
  * dims, B, L and lengths as given to r2l_gated_scan_train; dims->flags too.
- * Every sum runs in a fixed order: results are bitwise reproducible.
+ * Every sum runs in a fixed order: results are bitwise reproducible.  dr and
+ * dlam need σ(g) x a σ(r) / β within fp32's range before G multiplies it (|x|
+ * up to 1e37 where a memory is of 1000 positions).
  * workspace ≥ r2l_gated_scan_backward_workspace_size(dims, B, L) bytes,
  * 16-byte aligned; its first word is the device status word.                 */
 R2L_API r2l_status r2l_gated_scan_backward(const r2l_gated_in *in, const void *dy, int ld_dy, const float *dh_last,
@@ -483,7 +485,8 @@ R2L_API r2l_status r2l_gated_scan_backward(const r2l_gated_in *in, const void *d
  * for which every finite |x| of the group is ≤ 448 · 2^k.  The scale being a
  * power of two, a value that e4m3's 4 significant bits hold comes back as it
  * was, and packing what was unpacked changes nothing.  An infinity or a NaN
- * comes back as NaN.                                                         */
+ * comes back as NaN; |x| from 248 · 2^120 on, whose nearest value would be
+ * 2^128, is held as 240 · 2^120, so that finite values come back finite.     */
 #define R2L_ACT8_GROUP 64
 
 /* Packs x (dtype, [B·L, ldx], its first `cols` columns) into q ([B·L, ldq]

@@ -91,5 +91,6 @@ def act8_values(v):
         _, ue = np.frexp(u)
         grid = np.ldexp(1.0, np.maximum(ue - 1, -6) - 3)   # 3 fraction bits, and 2^-9 below the normal range
         q = np.ldexp(np.rint(u / grid) * grid, k)          # rint: ties to even
+        q = np.clip(q, -np.ldexp(240.0, 120), np.ldexp(240.0, 120))   # 256 * 2^120 is no fp32 number
         out[:, c:c + GROUP] = np.where(fine, q, np.nan)
     return out

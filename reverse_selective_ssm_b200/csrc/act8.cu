@@ -6,8 +6,9 @@
 // give a lane 8 channels of a row, 8 lanes a group; others are read element by
 // element, 32 neighbours at a time.  8 x 4096 rows of 2048 in bf16: pack 38 us
 // (5.3 TB/s), unpack 33 us (6.1 TB/s); of 8 x 2048 x 1037, whose rows start
-// anywhere, 51 and 22 us (1.0 and 2.3 TB/s).  Infinities and NaN are looked for
-// only where a group's largest bits say that there is one.
+// anywhere, 51 and 22 us (1.0 and 2.3 TB/s).  Infinities, NaN and values that
+// would round to 2^128 are looked for only where a group's largest bits say that
+// there is one.
 #include "act8.cuh"
 #include "gated_host.cuh"
 
@@ -105,12 +106,12 @@ __global__ void __launch_bounds__(WARPS * 32) act8_pack_wide_kernel(const T* x, 
     for (int k = 0; k < 8; ++k) top = max(top, __float_as_uint(e.v[k]) & 0x7fffffffu);
 #pragma unroll
     for (int d = 1; d < 8; d *= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-    const bool odd = __any_sync(0xffffffffu, top >= 0x7f800000u);
+    const bool odd = __any_sync(0xffffffffu, top >= r2l::act8::SPECIAL);
     if (odd) {     // an infinity or a NaN does not count for the scale
       top = 0;
       for (int k = 0; k < 8; ++k) {
         top = max(top, r2l::act8::finite_abs_bits(e.v[k]));
-        e.v[k] = r2l::act8::nan_if_not_finite(e.v[k]);
+        e.v[k] = r2l::act8::storable(e.v[k]);
       }
       for (int d = 1; d < 8; d *= 2) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
     }
@@ -149,10 +150,10 @@ __global__ void __launch_bounds__(WARPS * 32) act8_pack_kernel(const T* x, long 
     for (int g = 0; g < WGROUPS; ++g) {
       float a = v[j][2 * g], b = v[j][2 * g + 1];
       uint32_t top = __reduce_max_sync(0xffffffffu, max(__float_as_uint(a) & 0x7fffffffu, __float_as_uint(b) & 0x7fffffffu));
-      if (top >= 0x7f800000u) {     // an infinity or a NaN does not count for the scale
+      if (top >= r2l::act8::SPECIAL) {     // an infinity or a NaN does not count for the scale
         top = __reduce_max_sync(0xffffffffu, max(r2l::act8::finite_abs_bits(a), r2l::act8::finite_abs_bits(b)));
-        a = r2l::act8::nan_if_not_finite(a);
-        b = r2l::act8::nan_if_not_finite(b);
+        a = r2l::act8::storable(a);
+        b = r2l::act8::storable(b);
       }
       const uint32_t byte = r2l::act8::scale_byte(top);
       const float down = r2l::act8::scale_down(byte);

@@ -35,9 +35,15 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t max_bits) {
 __device__ __forceinline__ float scale_up(uint32_t byte) { return __uint_as_float(byte << 23); }            // 2^k
 __device__ __forceinline__ float scale_down(uint32_t byte) { return __uint_as_float((254u - byte) << 23); }  // 2^-k
 
-// NaN for an infinity or a NaN, v otherwise (e4m3 has no infinity, and the
-// conversion below would turn one into ±448).
-__device__ __forceinline__ float nan_if_not_finite(float v) { return v + (v - v); }
+// What is held of v: NaN for an infinity or a NaN (e4m3 has no infinity, and the
+// conversion below would turn one into ±448), and ±240 · 2^120 for finite values
+// from 248 · 2^120 on (the bits SPECIAL), which would be rounded to 2^128 and come
+// back as infinities.  Any other v as it is (its e4m3 value, that is): a group
+// without these two kinds needs no call.
+constexpr uint32_t SPECIAL = 0x7f780000u;
+__device__ __forceinline__ float storable(float v) {
+  return fminf(fmaxf(v, -240.0f * 0x1p120f), 240.0f * 0x1p120f) + (v - v);
+}
 
 // Two e4m3 bytes, `lo` in the low one, from values already divided by the scale.
 __device__ __forceinline__ uint16_t to_e4m3x2(float lo, float hi) {

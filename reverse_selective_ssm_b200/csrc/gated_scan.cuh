@@ -365,11 +365,11 @@ __device__ __forceinline__ void store_if(float* at, int j, int rows, float v) {
 // What an 8-bit checkpoint holds of values far out.  A gate beyond ±256 is kept
 // as ±256: its sigmoid is 0 or 1 in fp32 from ±104 on, and a mask of the type's
 // lowest value, or an infinity, leaves its scale's other channels the steps of
-// a group that reaches 256.  Other infinities become NaN.
+// a group that reaches 256.  x as in act8::storable.
 constexpr float GATE_MAX = 256.0f;
 constexpr uint32_t GATE_MAX_BITS = 0x43800000u;     // its bits
 __device__ __forceinline__ float storable(float v, bool gate) {
-  return !gate ? act8::nan_if_not_finite(v) : fabsf(v) > GATE_MAX ? copysignf(GATE_MAX, v) : v;
+  return !gate ? act8::storable(v) : fabsf(v) > GATE_MAX ? copysignf(GATE_MAX, v) : v;
 }
 __device__ __forceinline__ float2 storable(float2 v, bool gate) {
   return make_float2(storable(v.x, gate), storable(v.y, gate));
@@ -613,7 +613,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
                     0xffffffffu, VEC ? lane_abs_max(in + i * ARRAY + j * Lay::ROW, lane) : abs_max(value(i, j)));
               if (lane == i * ROWS + j) top = m;
             }
-          const bool odd = __any_sync(0xffffffffu, top >= (lane < ROWS ? 0x7f800000u : GATE_MAX_BITS + 1));
+          const bool odd = __any_sync(0xffffffffu, top >= (lane < ROWS ? act8::SPECIAL : GATE_MAX_BITS + 1));
           if (odd) {
 #pragma unroll 1
             for (int c = 0; c < 3 * ROWS; ++c) {

@@ -90,3 +90,54 @@ def test_gates_far_out_in_8_bits(E, fast, dtype):
     for k, v in out.items():
         assert bool(torch.isfinite(v.float()).all()), k
     check_backward(d, out, B, L, False, ("x8", "r8", "g8"))
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("cols", [128, 67])
+def test_finite_values_stay_finite_in_8_bits(cols, dtype):
+    """Values from 248 · 2^120 on would round to 256 · 2^120 = 2^128, which is no fp32 or bf16 number: they are held as
+    240 · 2^120, the largest that is."""
+    B, L, held = 1, 5, 240 * 2.0 ** 120
+    x = torch.randn(L, cols, generator=torch.Generator().manual_seed(44)).to(dtype)
+    big = torch.finfo(dtype).max
+    x[0, 0], x[0, 1], x[0, 2] = big, -big, 3e38
+    x[1, 3], x[1, 4] = 248 * 2.0 ** 120, -247 * 2.0 ** 120
+    x[2, 5], x[2, 6], x[2, 7] = -big, INF, float("nan")
+    x[3, 66] = big
+    q, s = bd.act8_pack(x.cuda(), B, L)
+    out = bd.act8_unpack(q, s, B, L, dtype).cpu()
+    assert out[0, 0] == held and out[0, 1] == -held and out[1, 3] == held and out[1, 4] == -held
+    assert out[2, 5] == -held and bool(torch.isnan(out[2, 6:8]).all()) and out[3, 66] == held
+    want = torch.from_numpy(O.act8_values(S.to_f64(x))).to(dtype)
+    nan = torch.isnan(want)
+    assert int(nan.sum()) == 2 and torch.equal(nan, torch.isnan(out)) and torch.equal(out[~nan], want[~nan])
+    q2, s2 = bd.act8_pack(out.cuda(), B, L)                 # packing what was unpacked changes nothing
+    again = bd.act8_unpack(q2, s2, B, L, dtype).cpu()
+    assert torch.equal(again[~nan], out[~nan]) and torch.equal(s, s2)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("E", [64, 67])
+def test_finite_inputs_stay_finite_in_a_scan_of_8_bits(E, dtype):
+    """The training forward packs as r2l_act8_pack does: its gradient is bit for bit that of the unpacked inputs.  dr and
+    dlam hold σ(g) x a σ(r) / β before G multiplies it, here up to 240 · 2^120 · 0.99 / 0.05 > 2^128, so an infinity
+    may stand there (in the same places of both); nothing else passes fp32's range."""
+    B, L = 2, 90
+    d = make(B, L, E, dtype, seed=45)
+    d["dy"], d["dh_last"] = (d["dy"] * 1e-6).to(dtype), d["dh_last"] * 1e-6
+    big = torch.finfo(dtype).max
+    d["x"][3::20, ::5], d["x"][7::20, 2::9] = big, -248 * 2.0 ** 120
+    c = dev(d)
+    _, _, ck, out = train(d, c, B, L, E, dtype, False, True)
+    full = bd.gated_dims(E, dtype)
+    back = {k: bd.act8_unpack(*bd.act8_pack(c[k], B, L), B, L, dtype) for k in ("x", "r", "g")}
+    assert all(bool(torch.isfinite(v).all()) for v in back.values())
+    same = bd.gated_scan_backward(c["dy"], c["lam"], full, B, L, ck[: bd.gated_scan_checkpoint_size(full, B, L)],
+                                  dh_last=c["dh_last"], **back)
+    for k, v in out.items():
+        assert torch.equal(v.nan_to_num(nan=7.0), same[k].nan_to_num(nan=7.0)), k
+        if k in ("dx", "dg", "dh0"):
+            assert bool(torch.isfinite(v).all()), k
+        else:                                               # channels without such an x
+            plain = ~(d["x"].abs() > 1e30).any(0).cuda()
+            assert bool(torch.isfinite(v[..., plain]).all()), k

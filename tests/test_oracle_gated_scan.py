@@ -108,3 +108,11 @@ def test_act8_values():
     np.testing.assert_array_equal(q[1, :64], 448.0)
     e = np.array([[1.0, -0.0625, 1.875, 448.0, np.inf, -np.inf, np.nan, 0.0, 17.0, 19.0]])
     np.testing.assert_array_equal(O.act8_values(e), [[1.0, -0.0625, 1.875, 448.0, np.nan, np.nan, np.nan, 0.0, 16.0, 20.0]])
+
+
+def test_act8_values_of_the_largest_numbers():
+    """Every finite fp32 number comes back as a finite one, and next to the border by e4m3's own steps."""
+    unit = 2.0 ** 120
+    v = np.array([[float(np.finfo(np.float32).max), -248 * unit, 248 * unit * (1 - 2.0 ** -24), 233 * unit, 232 * unit]])
+    np.testing.assert_array_equal(O.act8_values(v) / unit, [[240, -240, 240, 240, 224]])
+    assert np.all(np.isfinite(O.act8_values(v).astype(np.float32)))
