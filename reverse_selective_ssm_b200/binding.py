@@ -437,7 +437,18 @@ _CODES = {v: k for k, v in _DTYPES.items()}
 
 def gated_dims(channels: int, dtype: torch.dtype, flags: int = 0) -> Dims:
     """Dims of a gated scan over ``channels`` channels (the other fields are not read)."""
-    return Dims(channels, channels, 16, 1, 4, _CODES[dtype], flags)
+    return Dims(_int(channels), channels, 16, 1, 4, _CODES[dtype], flags)
+
+
+def _int(v: int) -> int:
+    """v, which the C interface takes as int (ctypes would pass its low 32 bits on)."""
+    if not -(1 << 31) <= v < 1 << 31:
+        raise ValueError(f"sizes are below 2^31, got {v}")
+    return v
+
+
+def _positions(B: int, L: int) -> int:
+    return _int(B) * _int(L)
 
 
 @contextlib.contextmanager
@@ -469,10 +480,11 @@ def _rows(t: torch.Tensor, M: int, E: int, dtype: torch.dtype, device: torch.dev
     if t.shape != (M, E) or t.dtype is not dtype or t.device != device:
         raise ValueError(f"{name} must be {dtype} [{M}, {E}] on {device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
     row, col = t.stride()
-    if M == 1 and row < E:
+    if M == 1:          # a stride that leads nowhere
         row = E
-    if (col != 1 and E > 1) or row < E:
-        raise ValueError(f"{name}: rows must be contiguous and must not overlap (strides {(row, col)})")
+    if (col != 1 and E > 1) or not E <= row < 1 << 31:
+        raise ValueError(f"{name}: rows must be contiguous and must not overlap, with a stride below 2^31 elements "
+                         f"(strides {(row, col)})")
     return t.data_ptr(), row
 
 
@@ -497,7 +509,7 @@ def _bytes(t: torch.Tensor, device: torch.device, name: str):
 def _gated_inputs(x, r, g, lam, h0, dims, B, L):
     if not x.is_cuda:
         raise ValueError("libr2l takes device tensors")
-    M, E, dtype, dev = B * L, dims.d_inner, _DTYPES[dims.dtype], x.device
+    M, E, dtype, dev = _positions(B, L), dims.d_inner, _DTYPES[dims.dtype], x.device
     px, ldx = _rows(x, M, E, dtype, dev, "x")
     pr, ldr = _rows(r, M, E, dtype, dev, "r")
     pg, ldg = _rows(g, M, E, dtype, dev, "g")
@@ -552,7 +564,7 @@ def gated_step(x: torch.Tensor, r: torch.Tensor, g: torch.Tensor, lam: torch.Ten
 
 
 def gated_scan_checkpoint_size(dims: Dims, B: int, L: int) -> int:
-    return int(load().r2l_gated_scan_checkpoint_size(ctypes.byref(dims), B, L))
+    return int(load().r2l_gated_scan_checkpoint_size(ctypes.byref(dims), _int(B), _int(L)))
 
 
 def gated_scan_train(x: torch.Tensor, r: torch.Tensor, g: torch.Tensor, lam: torch.Tensor, dims: Dims, B: int, L: int,
@@ -566,7 +578,7 @@ def gated_scan_train(x: torch.Tensor, r: torch.Tensor, g: torch.Tensor, lam: tor
 
 
 def gated_scan_backward_workspace_size(dims: Dims, B: int, L: int) -> int:
-    return int(load().r2l_gated_scan_backward_workspace_size(ctypes.byref(dims), B, L))
+    return int(load().r2l_gated_scan_backward_workspace_size(ctypes.byref(dims), _int(B), _int(L)))
 
 
 def gated_scan_backward(dy: torch.Tensor, lam: torch.Tensor, dims: Dims, B: int, L: int, checkpoint: torch.Tensor,
@@ -582,7 +594,7 @@ def gated_scan_backward(dy: torch.Tensor, lam: torch.Tensor, dims: Dims, B: int,
     lib = load()
     if not dy.is_cuda:
         raise ValueError("libr2l takes device tensors")
-    M, E, dtype, dev = B * L, dims.d_inner, _DTYPES[dims.dtype], dy.device
+    M, E, dtype, dev = _positions(B, L), dims.d_inner, _DTYPES[dims.dtype], dy.device
     if dims.flags & R2L_FLAG_ACT8:
         gi = GatedIn(None, None, None, 0, 0, 0, _vec(lam, (E,), dev, "lam"), None)
     else:
@@ -627,7 +639,7 @@ def act8_pack(x: torch.Tensor, B: int, L: int, lengths: Optional[torch.Tensor] =
         raise ValueError("libr2l takes device tensors")
     if x.dim() != 2 or x.dtype not in _CODES:
         raise ValueError("x must be [B·L, cols], bf16 or fp32")
-    M, cols, dev = B * L, x.shape[1], x.device
+    M, cols, dev = _positions(B, L), x.shape[1], x.device
     groups = -(-cols // ACT8_GROUP)
     px, ldx = _rows(x, M, cols, x.dtype, dev, "x")
 
@@ -657,7 +669,7 @@ def act8_unpack(q: torch.Tensor, scales: torch.Tensor, B: int, L: int, dtype: to
         raise ValueError("libr2l takes device tensors")
     if q.dim() != 2:
         raise ValueError("q must be [B·L, cols]")
-    M, cols, dev = B * L, q.shape[1], q.device
+    M, cols, dev = _positions(B, L), q.shape[1], q.device
     if out is not None:
         dtype = out.dtype
     if dtype not in _CODES:

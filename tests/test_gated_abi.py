@@ -177,3 +177,34 @@ def test_binding_takes_device_tensors_only(lib):
                  lambda: bd.gated_step(t, t, t, v, d, t), lambda: bd.act8_pack(t, 2, 2), lambda: bd.act8_unpack(t, v, 2, 2)):
         with pytest.raises(ValueError, match="device tensors"):
             call()
+
+
+def _strided(shape, strides, dtype=torch.bfloat16):
+    """A tensor of this layout without memory."""
+    return torch.empty_strided(shape, strides, dtype=dtype, device="meta")
+
+
+def test_binding_refuses_row_strides_past_31_bits():
+    """The C interface takes row strides as int: one of 2^32 + 64 elements must not arrive as 64."""
+    dev = torch.device("meta")
+    for stride in (2 ** 31, 2 ** 32 + 64, 2 ** 33 + 1):
+        with pytest.raises(ValueError, match="x: .*stride"):
+            bd._rows(_strided((2, 64), (stride, 1)), 2, 64, torch.bfloat16, dev, "x")
+    assert bd._rows(_strided((2, 64), (2 ** 31 - 1, 1)), 2, 64, torch.bfloat16, dev, "x")[1] == 2 ** 31 - 1
+    # one row has no distance to a next one
+    for stride in (0, 64, 100, 2 ** 32 + 64):
+        assert bd._rows(_strided((1, 64), (stride, 1)), 1, 64, torch.bfloat16, dev, "x")[1] == 64
+
+
+def test_binding_refuses_sizes_past_31_bits(lib):
+    """B and L are int in the C interface too: 2^32 + 1 positions must not arrive as one."""
+    d = _dims(E=1)
+    for B, L in ((2 ** 32 + 1, 1), (1, 2 ** 32 + 1), (2 ** 31, 1), (1, 2 ** 31)):
+        with pytest.raises(ValueError, match="2\\^31"):
+            bd._positions(B, L)
+        for size in (bd.gated_scan_checkpoint_size, bd.gated_scan_backward_workspace_size):
+            with pytest.raises(ValueError, match="2\\^31"):
+                size(d, B, L)
+    assert bd._positions(2 ** 31 - 1, 3) == 3 * (2 ** 31 - 1)
+    with pytest.raises(ValueError, match="2\\^31"):
+        bd.gated_dims(2 ** 32 + 64, torch.bfloat16)
