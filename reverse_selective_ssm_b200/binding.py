@@ -506,6 +506,16 @@ def _bytes(t: torch.Tensor, device: torch.device, name: str):
     return t.data_ptr(), t.numel() * t.element_size()
 
 
+def _status(t: Optional[torch.Tensor], device: torch.device) -> Optional[int]:
+    """Pointer of the device word that receives a call's status bits (None: not wanted)."""
+    if t is None:
+        return None
+    p, size = _bytes(t, device, "status")
+    if size < 4:
+        raise ValueError(f"status must hold a word of 4 bytes, got {size}")
+    return p
+
+
 def _gated_inputs(x, r, g, lam, h0, dims, B, L):
     if not x.is_cuda:
         raise ValueError("libr2l takes device tensors")
@@ -530,7 +540,7 @@ def _gated_forward(x, r, g, lam, dims, B, L, h0, lengths, checkpoint, y, h_last,
         py, ldy = _rows(y, B * L, E, x.dtype, dev, "y")
         ph = _vec(h_last, (B, E), dev, "h_last")
         pl = _vec(lengths, (B,), dev, "lengths", torch.int32)
-        ps = None if status is None else _bytes(status, dev, "status")[0]
+        ps = _status(status, dev)
         if not train:
             return lib.r2l_gated_scan(gi, py, ldy, ph, dims, B, L, pl, ps, st)
         if checkpoint is None:

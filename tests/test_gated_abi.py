@@ -208,3 +208,13 @@ def test_binding_refuses_sizes_past_31_bits(lib):
     assert bd._positions(2 ** 31 - 1, 3) == 3 * (2 ** 31 - 1)
     with pytest.raises(ValueError, match="2\\^31"):
         bd.gated_dims(2 ** 32 + 64, torch.bfloat16)
+
+
+def test_binding_refuses_a_status_without_room_for_a_word():
+    dev = torch.device("meta")
+    for n, dtype in ((0, torch.int32), (3, torch.uint8), (1, torch.int16)):
+        with pytest.raises(ValueError, match="status"):
+            bd._status(torch.empty(n, dtype=dtype, device=dev), dev)
+    for n, dtype in ((1, torch.int32), (4, torch.uint8)):
+        bd._status(torch.empty(n, dtype=dtype, device=dev), dev)
+    assert bd._status(None, dev) is None
