@@ -460,7 +460,9 @@ def _elsewhere(device: torch.device, stream):
             yield torch.cuda.current_stream(device).cuda_stream
         else:
             if not hasattr(stream, "cuda_stream"):
-                stream = torch.cuda.ExternalStream(int(stream), device=device)
+                # torch takes the handle 0 for a wish for a stream of its own
+                raw = int(stream)
+                stream = torch.cuda.ExternalStream(raw, device=device) if raw else torch.cuda.default_stream(device)
             with torch.cuda.stream(stream):
                 yield stream.cuda_stream
 

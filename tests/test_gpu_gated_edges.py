@@ -141,3 +141,21 @@ def test_finite_inputs_stay_finite_in_a_scan_of_8_bits(E, dtype):
         else:                                               # channels without such an x
             plain = ~(d["x"].abs() > 1e30).any(0).cuda()
             assert bool(torch.isfinite(v[..., plain]).all()), k
+
+
+def test_the_default_stream_by_its_raw_handle():
+    """stream=0 is the device's default stream, as cudaStream_t has it, not another one."""
+    assert torch.cuda.default_stream().cuda_stream == 0
+    device = torch.device("cuda", torch.cuda.current_device())
+    with bd._elsewhere(device, 0) as raw:
+        assert raw == 0 and torch.cuda.current_stream().cuda_stream == 0
+    B, L, E = 2, 40, 64
+    d = make(B, L, E, FP32, seed=46)
+    c = dev(d)
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):                           # another stream being the current one
+        torch.cuda.synchronize()
+        y, h, _, out = train(d, c, B, L, E, FP32, False, False, stream=0)
+        torch.cuda.synchronize()
+    check_forward(d, y, h, B, L, False)
+    check_backward(d, out, B, L, False)
