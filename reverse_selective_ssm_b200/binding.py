@@ -473,6 +473,8 @@ def _call_on(device: torch.device, stream, f):
     asked for directly: contexts and stream objects cost more than the launch of a decoding step."""
     if stream is None and device.index == torch.cuda.current_device():
         return f(torch._C._cuda_getCurrentRawStream(device.index))
+    if getattr(stream, "device", device) != device:
+        raise ValueError(f"the stream is on {stream.device}, the tensors are on {device}")
     with _elsewhere(device, stream) as st:
         return f(st)
 

@@ -218,3 +218,14 @@ def test_binding_refuses_a_status_without_room_for_a_word():
     for n, dtype in ((1, torch.int32), (4, torch.uint8)):
         bd._status(torch.empty(n, dtype=dtype, device=dev), dev)
     assert bd._status(None, dev) is None
+
+
+def test_binding_refuses_a_stream_of_another_device():
+    class Elsewhere:
+        device, cuda_stream = torch.device("cuda", 1), 0x40
+
+    def never(raw):
+        raise AssertionError("called")
+
+    with pytest.raises(ValueError, match="stream"):
+        bd._call_on(torch.device("cuda", 0), Elsewhere(), never)
