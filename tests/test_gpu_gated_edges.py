@@ -1,5 +1,6 @@
-"""Calls at the edges of what the gated scan and the 8-bit checkpoints accept: parameters without bounds, gates far out
-and values near a type's largest, on the GPU against the float64 oracle (tolerances as in test_gpu_gated_scan.py)."""
+"""Calls at the edges of what the gated scan and the 8-bit checkpoints accept: parameters without bounds, gates far out,
+values near a type's largest, the default stream by its handle; and a hook's gradient from 8 bits.  On the GPU against the
+float64 oracle (tolerances as in test_gpu_gated_scan.py and test_gpu_hook_backward.py)."""
 import numpy as np
 import pytest
 import torch
@@ -8,6 +9,7 @@ import oracle as O
 from reverse_selective_ssm_b200 import binding as bd
 from reverse_selective_ssm_b200 import synthetic as S
 
+from . import test_gpu_hook_backward as HB
 from .test_gpu_gated_scan import check_backward, check_forward, dev, flags_of, lengths_tensor, make, train
 
 pytestmark = pytest.mark.gpu
@@ -159,3 +161,26 @@ def test_the_default_stream_by_its_raw_handle():
         torch.cuda.synchronize()
     check_forward(d, y, h, B, L, False)
     check_backward(d, out, B, L, False)
+
+
+def test_hook_gradient_from_8_bits_is_the_formula_at_what_they_hold():
+    """A hook's whole gradient from a hidden state kept in 8 bits, against the oracle's gradient at the values that the
+    8 bits stand for (bf16 holds them exactly), within the bf16 path's 2e-2; rows of 136 channels end in a short group.
+    It is that gradient and not the exact hidden state's: bf16 is off by 2^-8 of a value, e4m3 by 2^-4, so the kernels'
+    is nearer to the oracle's at the held values than half of what lies between the oracle's two."""
+    dims = S.Dims(d_model=136, d_inner=192, d_state=16, dt_rank=8, d_conv=4)
+    lengths = torch.tensor([75, 38], dtype=torch.int32)
+    dims, h, w, dh_out = HB.make(2, 75, seed=47, lengths=lengths, dims=dims)
+    B, L, E = h.shape
+    flat, lt = h.cuda().view(B * L, E), lengths.cuda()
+    q, s = bd.act8_pack(flat, B, L, lengths=lt)
+    held = torch.full_like(flat, float("nan"))              # padding rows are not read
+    bd.act8_unpack(q, s, B, L, lengths=lt, out=held)
+    got = HB.run_gpu(dims, held.view(B, L, E).cpu(), w, 0.7, dh_out, lengths)
+    exact = torch.from_numpy(O.act8_values(S.to_f64(h.view(B * L, E)))).to(h.dtype).view(B, L, E)
+    want = HB.run_oracle(exact, w, 0.7, dh_out, lengths)
+    HB.compare(got, want, h, dh_out, lengths)
+    other = HB.run_oracle(h, w, 0.7, dh_out, lengths)
+    for k in ("W_in", "W_x", "W_out"):
+        between = np.linalg.norm(want["d" + k] - other["d" + k])
+        assert np.linalg.norm(S.to_f64(got[2][k]) - want["d" + k]) < between / 2, k
