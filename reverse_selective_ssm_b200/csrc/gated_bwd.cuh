@@ -13,7 +13,9 @@
 // issue slots are used: 397 us, 4.8 TB/s.  In fp32 (8 x 2048 x 4096) 313 us,
 // 6.0 TB/s.  From 8-bit rows it reads 3 bytes less and spends 14 instructions
 // more on them: 445 us.  168 registers and 12 warps: 422 us.  Gradients staged
-// in shared memory and written 16 bytes a lane: 407 us.
+// in shared memory and written 16 bytes a lane: 407 us.  Rows that start anywhere
+// are copied element by element; whole pieces were measured in fp32 alone, in
+// blocks bound to 128 registers (5 ragged x 777 x 515: 27 us, and 44 with pieces).
 #pragma once
 
 #include "gated_scan.cuh"
@@ -23,31 +25,6 @@ namespace gated {
 
 constexpr float TINY = 1.17549435e-38f;
 constexpr int BL = 16;                     // lanes of a row
-
-// One element to shared memory, or 0 where it does not exist (`from` is valid all the same).
-__device__ __forceinline__ void copy_element(float* to, const float* from, bool exists) {
-  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_addr(to)), "l"(from), "r"(exists ? 4 : 0) : "memory");
-}
-__device__ __forceinline__ void copy_element(bf16* to, const bf16* from, bool exists) {
-  *to = exists ? *from : from_f32<bf16>(0.0f);
-}
-
-// Rows that start anywhere, of which `cols` channels exist (the others are 0),
-// element by element: whole 16-byte pieces (copy_any) cost registers that the
-// gradient has not (5 ragged x 777 x 515, fp32: 27 us, and 44 with pieces);
-// `first` is position 0 at the block's first channel.
-template <typename T, typename LAY>
-__device__ __forceinline__ void copy_elements(T* dst, const T* first, int step, int k, int n, int cols, int wl) {
-  static_assert(LAY::CHANNELS % 32 == 0, "a lane copies a channel");
-#pragma unroll
-  for (int c = 0; c < LAY::CHANNELS; c += 32) {
-    const bool exists = c + wl < cols;
-    const T* const from = first + (exists ? c + wl : 0);
-#pragma unroll 8
-    for (int row = 0; row < LAY::WARP_ROWS; ++row)
-      copy_element(dst + LAY::at(row) + c + wl, from + (long long)min(k + row, n - 1) * step, exists);
-  }
-}
 
 template <typename T, bool ACT8, int WARPS>
 struct BwdSmem {

@@ -36,7 +36,7 @@ r2l_status launch_shape(const FwdArgs& p, uint32_t blocks, cudaStream_t st) {
   using namespace r2l::gated;
   const long long jobs = (long long)p.B * ((p.E - 1) / (2 * LANES) + 1);
   return launch(gated_scan_kernel<T, VEC, MODE, LANES, WARPS>, p, jobs, blocks, WARPS * 32,
-                fwd_smem_bytes<T, VEC, LANES, WARPS>(blocks), st);
+                fwd_smem_bytes<T, WHOLE_PIECES<T, VEC, MODE, WARPS>, LANES, WARPS>(blocks), st);
 }
 template <typename T, bool VEC, int MODE>
 r2l_status launch_forward(const FwdArgs& p, Split c, cudaStream_t st) {

@@ -292,8 +292,7 @@ __device__ __forceinline__ Edges array_edges(int b, int B, int n, int L, bool fo
 // reach outside it, go element by element, as do rows shorter than a piece.
 // `first` is position 0 at the block's first channel, of which `cols` exist.
 // All rows element by element: 61 ragged x 512 x 1037, fp32, 100 us, here 70;
-// 8 x 2000 x 1037, bf16, 86 and 53.  The 8-bit forward of 5 ragged x
-// 777 x 515, fp32, loses by it, 27 us and 30.
+// 8 x 2000 x 1037, bf16, 86 and 53.
 template <typename T, typename LAY>
 __device__ __forceinline__ void copy_any(T* dst, const T* first, int step, int k, int n, int cols, const Edges& edges, int wl) {
   constexpr int PIECES = LAY::CHUNKS + 1;
@@ -312,6 +311,29 @@ __device__ __forceinline__ void copy_any(T* dst, const T* first, int step, int k
     }
   }
 }
+// One element to shared memory, or 0 where it does not exist (`from` is valid all the same).
+__device__ __forceinline__ void copy_element(float* to, const float* from, bool exists) {
+  asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(smem_addr(to)), "l"(from), "r"(exists ? 4 : 0) : "memory");
+}
+__device__ __forceinline__ void copy_element(bf16* to, const bf16* from, bool exists) {
+  *to = exists ? *from : from_f32<bf16>(0.0f);
+}
+
+// copy_elements: the same rows element by element, into rows of shared memory
+// that start at their channel 0, with 0 in channels that do not exist.
+template <typename T, typename LAY>
+__device__ __forceinline__ void copy_elements(T* dst, const T* first, int step, int k, int n, int cols, int wl) {
+  static_assert(LAY::CHANNELS % 32 == 0, "a lane copies a channel");
+#pragma unroll
+  for (int c = 0; c < LAY::CHANNELS; c += 32) {
+    const bool exists = c + wl < cols;
+    const T* const from = first + (exists ? c + wl : 0);
+#pragma unroll 8
+    for (int row = 0; row < LAY::WARP_ROWS; ++row)
+      copy_element(dst + LAY::at(row) + c + wl, from + (long long)min(k + row, n - 1) * step, exists);
+  }
+}
+
 // v in all channels of the rows from `rows` on, of a warp that has no more.
 template <typename T, typename LAY>
 __device__ __forceinline__ void fill_rows(T* dst, int wl, int rows, float v) {
@@ -494,24 +516,34 @@ __device__ __forceinline__ float2 other_half(float2 v) {
 
 constexpr int ROWS = 8;      // consecutive rows of a thread
 
+// Whether rows that start anywhere come in whole pieces.  The 8-bit forward in
+// fp32 has no registers to spare: in blocks of 8 warps it spills with them and
+// takes 29.1 us of 5 ragged x 777 x 515 (by elements 26.6), 68.5 of 16 x 1000 x
+// 515 (60.7) and 128 of 8 x 2000 x 1037 (115).  In blocks of 4 warps pieces are
+// ahead all the same (61 x 512 x 1037: 181 us and 189), and so they are in bf16
+// (8 x 2000 x 1037: 116 us and 125).
+template <typename T, bool VEC, int MODE, int WARPS>
+constexpr bool WHOLE_PIECES = !VEC && !(MODE == 2 && sizeof(T) == 4 && WARPS == 8);
+
 // In shared memory, behind it the maps of the cluster's blocks, [2][blocks][LANES].
-template <typename T, bool VEC, int LANES, int WARPS>
+template <typename T, bool ANY, int LANES, int WARPS>
 struct FwdSmem {
-  T in[2][3][WARPS * Layout<T, LANES, ROWS, !VEC>::WARP_STRIDE];
+  T in[2][3][WARPS * Layout<T, LANES, ROWS, ANY>::WARP_STRIDE];
   float4 maps[2][WARPS][LANES];
   float2 carry[WARPS][LANES];
 };
-template <typename T, bool VEC, int LANES, int WARPS>
+template <typename T, bool ANY, int LANES, int WARPS>
 constexpr size_t fwd_smem_bytes(uint32_t blocks) {
-  return sizeof(FwdSmem<T, VEC, LANES, WARPS>) + (blocks > 1 ? 2 * sizeof(float4) * LANES * blocks : 0);
+  return sizeof(FwdSmem<T, ANY, LANES, WARPS>) + (blocks > 1 ? 2 * sizeof(float4) * LANES * blocks : 0);
 }
 
 // MODE 0: the recurrence; 1: also the states of a checkpoint; 2: and its 8 bits.
 template <typename T, bool VEC, int MODE, int LANES, int WARPS>
 __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
     gated_scan_kernel(const FwdArgs p, const uint32_t blocks) {
-  typedef Layout<T, LANES, ROWS, !VEC> Lay;
-  typedef FwdSmem<T, VEC, LANES, WARPS> Smem;
+  constexpr bool ANY = WHOLE_PIECES<T, VEC, MODE, WARPS>;
+  typedef Layout<T, LANES, ROWS, ANY> Lay;
+  typedef FwdSmem<T, ANY, LANES, WARPS> Smem;
   static_assert(MODE < 2 || LANES == 32, "the channels of a scale are a row of the warp");
   constexpr int SPAN = WARPS * Lay::WARP_ROWS;      // rows of the block's tile
   extern __shared__ __align__(16) unsigned char smem_raw[];
@@ -551,10 +583,14 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
         copy_rows<T, Lay>(to + ARRAY * (int)sizeof(T), r0, r_step, k, n, wl, exists);
         copy_rows<T, Lay>(to + 2 * ARRAY * (int)sizeof(T), g0, g_step, k, n, wl, exists);
       } else {
+        auto copy = [&](T* to, const T* first, int step) {
+          if constexpr (ANY) copy_any<T, Lay>(to, first, step, k, n, cols, edges, wl);
+          else copy_elements<T, Lay>(to, first, step, k, n, cols, wl);
+        };
         T* const to = rows0 + buf * 3 * ARRAY;
-        copy_any<T, Lay>(to, x0, x_step, k, n, cols, edges, wl);
-        copy_any<T, Lay>(to + ARRAY, r0, r_step, k, n, cols, edges, wl);
-        copy_any<T, Lay>(to + 2 * ARRAY, g0, g_step, k, n, cols, edges, wl);
+        copy(to, x0, x_step);
+        copy(to + ARRAY, r0, r_step);
+        copy(to + 2 * ARRAY, g0, g_step);
       }
     }
     copies_commit();
@@ -578,11 +614,11 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
       copies_wait<1>();
       __syncwarp();
       // rows that start anywhere: where this group's first ones do (rows past the end are filled from any start)
-      const int first = k + half * ROWS, x_offset = VEC ? 0 : offset_of(x0, x_step, first),
-                r_offset = VEC ? 0 : offset_of(r0, r_step, first), g_offset = VEC ? 0 : offset_of(g0, g_step, first);
+      const int first = k + half * ROWS, x_offset = !ANY ? 0 : offset_of(x0, x_step, first),
+                r_offset = !ANY ? 0 : offset_of(r0, r_step, first), g_offset = !ANY ? 0 : offset_of(g0, g_step, first);
       auto value = [&](int i, int j) {      // x, r or g of row j of this group
         const T* const at = in + i * ARRAY + j * Lay::ROW;
-        if constexpr (VEC) return lane_pair(at, lane);
+        if constexpr (!ANY) return lane_pair(at, lane);
         const uint32_t offset = (i == 0 ? x_offset : i == 1 ? r_offset : g_offset) +
                                 (uint32_t)j * (uint32_t)(i == 0 ? x_step : i == 1 ? r_step : g_step);
         return any_pair(at + (offset & (Lay::PER - 1)), lane, cols);
@@ -610,7 +646,7 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
 #pragma unroll
             for (int j = 0; j < ROWS; ++j) {
               const uint32_t m = __reduce_max_sync(
-                    0xffffffffu, VEC ? lane_abs_max(in + i * ARRAY + j * Lay::ROW, lane) : abs_max(value(i, j)));
+                    0xffffffffu, !ANY ? lane_abs_max(in + i * ARRAY + j * Lay::ROW, lane) : abs_max(value(i, j)));
               if (lane == i * ROWS + j) top = m;
             }
           const bool odd = __any_sync(0xffffffffu, top >= (lane < ROWS ? act8::SPECIAL : GATE_MAX_BITS + 1));

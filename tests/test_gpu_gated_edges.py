@@ -184,3 +184,28 @@ def test_hook_gradient_from_8_bits_is_the_formula_at_what_they_hold():
     for k in ("W_in", "W_x", "W_out"):
         between = np.linalg.norm(want["d" + k] - other["d" + k])
         assert np.linalg.norm(S.to_f64(got[2][k]) - want["d" + k]) < between / 2, k
+
+
+@pytest.mark.parametrize("E", [1, 3, 31, 67, 129])
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
+def test_long_rows_that_start_anywhere_among_nan_in_8_bits(dtype, E):
+    """The training forward with 8-bit copies, and its gradient, on long sequences whose rows lie in buffers of NaN, each
+    with its own start and distance: what lies beside a row counts neither for the states nor for a scale."""
+    B, L = 2, 700
+    d = make(B, L, E, dtype, seed=48 + E, lens=[700, 333])
+    c = dev(d)
+
+    def among_nan(t, start, gap):
+        buf = torch.full((start + B * L * (E + gap) + 9,), float("nan"), dtype=dtype, device="cuda")
+        at = buf.as_strided((B * L, E), (E + gap, 1), start)
+        at.copy_(t)
+        return at
+
+    for forward in (False, True):
+        y0, h0, ck0, out0 = train(d, c, B, L, E, dtype, forward, True)
+        check_forward(d, y0, h0, B, L, forward)
+        for start, gap in ((1, 1), (7, 4)):
+            e = dict(c, **{k: among_nan(c[k], start + j, gap + j) for j, k in enumerate(("x", "r", "g", "dy"))})
+            y, h, _, out = train(d, e, B, L, E, dtype, forward, True)
+            check_forward(d, y, h, B, L, forward)
+            assert torch.equal(h, h0) and all(torch.equal(out[k], out0[k]) for k in out)
