@@ -49,8 +49,16 @@ __device__ __forceinline__ float2 near_beta_inverse(float2 l2) {
   return __ffma2_rn(c, l2, two(1.0f));
 }
 
+// Warps of an SM that a thread's registers have to leave room for.  fp32 rows of
+// 8 warps fill 145 KB of shared memory, so one block is all that an SM holds,
+// whatever its registers: where rows start anywhere it may have them all (246,
+// and no spills; 16 x 1000 x 515: 88 -> 78 us, 5 ragged x 777 x 515: 26.8 -> 25.8);
+// on 16-byte boundaries 128 are enough (8 x 2048 x 4096: 310 us, and 312 with 252).
 template <typename T, bool VEC, bool ACT8, int WARPS>
-__global__ void __launch_bounds__(WARPS * 32, (sizeof(T) == 2 || WARPS == 8 ? 16 : 12) / WARPS)
+constexpr int BWD_WARPS = sizeof(T) == 2 ? 16 : WARPS == 4 ? 12 : ACT8 || VEC ? 16 : 8;
+
+template <typename T, bool VEC, bool ACT8, int WARPS>
+__global__ void __launch_bounds__(WARPS * 32, BWD_WARPS<T, VEC, ACT8, WARPS> / WARPS)
     gated_bwd_kernel(const BwdArgs p, const uint32_t blocks) {
   typedef BwdSmem<T, ACT8, WARPS> Smem;
   typedef typename Smem::Q Q;
