@@ -428,8 +428,8 @@ typedef struct {
  * status: device word that receives the R2L_DEVFLAG_* bits of this call (what
  * r2l_get_device_status reads), or NULL.  No workspace is needed, and nothing
  * is enqueued on an error.  A sequence's result does not depend on the other
- * sequences' values; it is bitwise reproducible for given B, L and E, which
- * choose how the work is cut.                                                */
+ * sequences' values; it is bitwise reproducible for given B, L and E and
+ * lengths given or not, which choose how the work is cut.                    */
 R2L_API r2l_status r2l_gated_scan(const r2l_gated_in *in, void *y, int ldy, float *h_last, const r2l_dims *dims,
                                   int B, int L, const int32_t *lengths, uint32_t *status, void *stream);
 
@@ -466,9 +466,10 @@ R2L_API size_t r2l_gated_scan_backward_workspace_size(const r2l_dims *dims, int 
  * the gradient is then the formula at the values that the checkpoint's 8 bits
  * stand for, each tile's states recomputed from its exact first one.
  * dims, B, L and lengths as given to r2l_gated_scan_train; dims->flags too.
- * Every sum runs in a fixed order: results are bitwise reproducible.  dr and
- * dlam need σ(g) x a σ(r) / β within fp32's range before G multiplies it (|x|
- * up to 1e37 where a memory is of 1000 positions).
+ * Every sum runs in a fixed order: results are bitwise reproducible (with
+ * lengths and without, a call may be cut differently).  dr and dlam need
+ * σ(g) x a σ(r) / β within fp32's range before G multiplies it (|x| up to 1e37
+ * where a memory is of 1000 positions).
  * workspace ≥ r2l_gated_scan_backward_workspace_size(dims, B, L) bytes,
  * 16-byte aligned; its first word is the device status word.                 */
 R2L_API r2l_status r2l_gated_scan_backward(const r2l_gated_in *in, const void *dy, int ld_dy, const float *dh_last,

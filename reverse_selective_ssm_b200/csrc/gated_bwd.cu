@@ -1,4 +1,6 @@
 // Entry point of the gated recurrence's gradient.
+#include <algorithm>
+
 #include "gated_bwd.cuh"
 #include "gated_host.cuh"
 
@@ -10,12 +12,18 @@ namespace {
 // Blocks of 4 warps (64 positions of 32 channels); of 8 warps where few blocks
 // have long sequences, and for long ones in fp32, whose rows are what bounds it
 // (8 x 2048 x 4096, fp32: 346 us with 4 warps, 313 with 8; bf16, 8 x 4096 x
-// 4096: 398 and 418; one sequence of 2048 x 4096: 58 and 44).
-Split backward_split(const r2l_dims* d, int B, int L) {
+// 4096: 398 and 418; one sequence of 2048 x 4096: 58 and 44).  Clusters are
+// the same from 8-bit rows as from full ones, whose gradient is cut alike and so
+// the same bit for bit.  fp32 rows fill an SM's shared memory with one block, and
+// clusters of 2 that do not all fit cost more than they bring (one sequence of
+// 2048 x 3040, 95 blocks: single 46 us, clusters of 2 66; 5 x 777 x 520 23.5 and
+// 34.8), unless lengths are given: blocks of short sequences make room (the same,
+// ragged, 23.6 and 21.7).
+Split backward_split(const r2l_dims* d, int B, int L, bool lengths) {
   const long long jobs = (long long)B * ((d->d_inner - 1) / 32 + 1);
-  const bool wide_rows = d->dtype == R2L_FP32 && !(d->flags & R2L_FLAG_ACT8);
-  if (L >= 512 && (jobs <= 296 || (wide_rows && L >= 1024))) return {cluster_of(jobs, 128, L, 190), 8};
-  return {1, 4};
+  const bool fp32 = d->dtype == R2L_FP32, wide_rows = fp32 && !(d->flags & R2L_FLAG_ACT8);
+  if (L < 512 || (jobs > 296 && !(wide_rows && L >= 1024))) return {1, 4};
+  return {cluster_of(jobs, 128, L, fp32 ? Clusters{190, 190, lengths ? 190 : 148} : Clusters{256, 256, 190}), 8};
 }
 
 template <typename T, bool VEC, bool ACT8>
@@ -27,8 +35,10 @@ r2l_status run_backward(const BwdArgs& p, Split c, cudaStream_t st) {
   return launch(gated_bwd_kernel<T, VEC, ACT8, 8>, p, jobs, c.blocks, 256, bwd_smem_bytes<T, ACT8, 8>(c.blocks), st);
 }
 
-// Rows of the shares of dlam, and of their sums where one launch does not add them all.
-long long part_rows(const r2l_dims* d, int B, int L) { return (long long)B * backward_split(d, B, L).blocks; }
+// Rows of the shares of dlam (the most that a call may have), and of their sums where one launch does not add them all.
+long long part_rows(const r2l_dims* d, int B, int L) {
+  return (long long)B * std::max(backward_split(d, B, L, false).blocks, backward_split(d, B, L, true).blocks);
+}
 long long sum_rows(long long rows) { return rows > DLAM_ROWS ? (rows - 1) / DLAM_ROWS + 1 : 0; }
 size_t part_bytes(const r2l_dims* d, int B, int L) {
   const long long rows = part_rows(d, B, L);
@@ -92,7 +102,7 @@ r2l_status r2l_gated_scan_backward(const r2l_gated_in* in, const void* dy, int l
   const bool vec = E * es % 16 == 0 && (act8 || (rows16(p.x, p.ldx, es) && rows16(p.r, p.ldr, es) && rows16(p.g, p.ldg, es))) &&
                    rows16(p.dy, p.ld_dy, es) && rows16(p.dx, p.ld_dx, es) && rows16(p.dr, p.ld_dr, es) &&
                    rows16(p.dg, p.ld_dg, es);
-  const Split c = backward_split(dims, B, L);
+  const Split c = backward_split(dims, B, L, lengths != nullptr);
   cudaStream_t st = (cudaStream_t)stream;
   if (dims->dtype == R2L_BF16) {
     if (act8) R2L_TRY((vec ? run_backward<bf16, true, true> : run_backward<bf16, false, true>)(p, c, st));
@@ -101,7 +111,7 @@ r2l_status r2l_gated_scan_backward(const r2l_gated_in* in, const void* dy, int l
     if (act8) R2L_TRY((vec ? run_backward<float, true, true> : run_backward<float, false, true>)(p, c, st));
     else R2L_TRY((vec ? run_backward<float, true, false> : run_backward<float, false, false>)(p, c, st));
   }
-  const int width = p.strips * STRIP, rows = (int)part_rows(dims, B, L), sums = (int)sum_rows(rows);
+  const int width = p.strips * STRIP, rows = (int)(B * (long long)c.blocks), sums = (int)sum_rows(rows);
   const dim3 by_channels((E + 31) / 32);
   if (sums) {
     float* const more = p.part + (size_t)rows * width;

@@ -90,15 +90,34 @@ struct Split {
   uint32_t blocks;
   int warps;
 };
-// Blocks of 8 warps that number few: clusters of up to 8 of them, as long as
-// all clusters together stay within `most` blocks and a round within L.  A
-// round of a cluster costs a barrier of about 1.2 us, which pays only where
-// SMs would be idle otherwise (one sequence of 8192 x 256 channels: 58 us with
-// single blocks, 21 us with clusters of 8; one of 2048 x 4096: 19 us and 37).
-inline uint32_t cluster_of(long long jobs, int rows, int L, long long most) {
-  uint32_t c = 1;
-  while (c < (uint32_t)MAX_CLUSTER && jobs * c * 2 <= most && (long long)rows * c * 2 < 2LL * L) c *= 2;
-  return c;
+// Clusters of blocks of 8 warps: the most blocks that clusters of 8, 4 and 2 may
+// number (0: no such clusters).
+struct Clusters {
+  int of8, of4, of2;
+};
+// The largest clusters within these limits whose rounds stay within L.  A round
+// of a cluster costs a barrier of about 1.2 us where single blocks hand the state
+// from warp to warp, and clusters that cannot all run at once cost a second wave
+// (a cluster lies within one of the chip's groups of SMs, so not every SM can be
+// part of one): at two blocks an SM 256 blocks in clusters run at once.
+// One sequence of 4096 x 512, 1024, 2048, 3040 and 4096 channels, bf16, scan:
+//   single blocks  32.0  32.6  33.0  33.8  34.5 us
+//   clusters of 2  36.2  37.1  38.8  46.0  47.9
+//   clusters of 4  20.7  22.4  27.6  46.4  53.6
+//   clusters of 8  15.0  17.2  31.7  47.1  61.7
+// and its gradient:
+//   single blocks  76.3  77.6  78.4  78.9  79.2
+//   clusters of 2  53.3  53.9  55.3  74.4  75.7
+//   clusters of 4  29.9  31.3  43.8  68.3  81.7
+//   clusters of 8  24.2  27.0  51.1  71.0  91.3
+inline uint32_t cluster_of(long long jobs, int rows, int L, Clusters most) {
+  const int limits[] = {most.of8, most.of4, most.of2};
+  uint32_t c = MAX_CLUSTER;
+  for (int limit : limits) {
+    if (jobs * c <= limit && (long long)rows * c < 2LL * L) return c;
+    c /= 2;
+  }
+  return 1;
 }
 
 template <typename Args>

@@ -16,17 +16,26 @@ namespace {
 // are more than one wave of blocks: less of a block's life is its first tile.
 // Measured, 4 and 8 warps: 8 x 4096 x 4096 channels 204 and 183 us, 8 x 128 x
 // 4096 11 and 16 us, 256 ragged sequences of up to 512 389 and 632 us.
-Split forward_split(int B, int E, int L, int mode) {
-  const long long jobs64 = (long long)B * ((E - 1) / 64 + 1);
+// Clusters of 2 do not pay here, the barrier undoes what a second block brings,
+// except in ragged batches of odd rows, whose copies take longer (5 ragged x 777 x
+// 515, fp32: single 20.1 us, clusters of 2 18.8; all of full length 21.3 and 34.7).
+// fp32 rows are nearer to what memory gives, so fewer clusters of 4 pay (64 blocks
+// of 600 positions: single 9.4 us, clusters of 4 11.5), and with their 8-bit copies
+// clusters of 8 leave shared memory for one block an SM (one sequence of 2048 x
+// 2048, 32 blocks: 49.9 us, clusters of 4 33.1).
+Split forward_split(int B, int E, int L, int mode, int size, bool lengths) {
+  const long long jobs64 = (long long)B * ((E - 1) / 64 + 1), jobs32 = (long long)B * ((E - 1) / 32 + 1);
   if (L < 512 || (L < 1024 && jobs64 > 592)) return {1, 4};
-  return {mode == 2 ? cluster_of(jobs64, 64, L, 256) : cluster_of((long long)B * ((E - 1) / 32 + 1), 128, L, 190), 8};
+  if (mode == 2) return {cluster_of(jobs64, 64, L, {size == 2 ? 256 : 96, 256, 0}), 8};
+  return {cluster_of(jobs32, 128, L, {256, size == 2 ? 256 : 192, lengths && E % (16 / size) ? 190 : 0}), 8};
 }
 
 // Whether every thread walks a sequence by itself: steps of one or two
-// positions (2 positions of 8 x 1024 channels 3.2 us, in tiles 3.8; 4 positions
-// 4.5 and 3.5), and short pieces of so many channels that tiles, filled by 8
-// positions to a quarter, would take several waves (8192 sequences of 4 x 4096
-// channels 209 us, in tiles 622; 12 positions 192 and 220, 16 195 and 143).
+// positions (2 positions of 8 x 1024 channels 3.1 us, in tiles 3.7; 4 positions
+// 4.4 and 3.5), and short pieces of so many channels that tiles, filled by 8
+// positions to a quarter, would take several waves (8192 rows of 4096 channels in
+// pieces of 4 positions 117 us, in tiles 618; of 12 112 and 218, of 16 116 and
+// 142, of 24 126 and 103).
 bool walks(int B, int E, int L) {
   return L <= 2 || (L <= 16 && (long long)B * ((E - 1) / 64 + 1) > 592);
 }
@@ -56,7 +65,7 @@ r2l_status run_forward(const FwdArgs& p, int mode, cudaStream_t st) {
     R2L_LAUNCH_CHECK();
     return R2L_OK;
   }
-  const Split c = forward_split(p.B, p.E, p.L, mode);
+  const Split c = forward_split(p.B, p.E, p.L, mode, sizeof(T), p.lengths != nullptr);
   if (mode == 0) return launch_forward<T, VEC, 0>(p, c, st);
   return mode == 1 ? launch_forward<T, VEC, 1>(p, c, st) : launch_forward<T, VEC, 2>(p, c, st);
 }

@@ -209,3 +209,22 @@ def test_long_rows_that_start_anywhere_among_nan_in_8_bits(dtype, E):
             y, h, _, out = train(d, e, B, L, E, dtype, forward, True)
             check_forward(d, y, h, B, L, forward)
             assert torch.equal(h, h0) and all(torch.equal(out[k], out0[k]) for k in out)
+
+
+@pytest.mark.parametrize("act8", [False, True], ids=["full", "act8"])
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("B,L,E,lens", [(1, 1100, 500, None), (1, 1100, 1000, None), (2, 1100, 1030, [1100, 514]),
+                                        (1, 1100, 3040, None), (5, 777, 515, [777, 0, 388, 583, 194]), (2, 600, 512, [0, 600])])
+def test_every_choice_of_clusters(B, L, E, lens, dtype, act8):
+    """Few channels and long sequences: single blocks and clusters of every size, of full length and ragged."""
+    d = make(B, L, E, dtype, seed=50, lens=lens)
+    c = dev(d)
+    y, h, _, out = train(d, c, B, L, E, dtype, False, act8)
+    check_forward(d, y, h, B, L, False)
+    if act8:
+        for k in ("x", "r", "g"):
+            d[k + "8"] = torch.from_numpy(O.act8_values(S.to_f64(d[k])))
+    check_backward(d, out, B, L, False, ("x8", "r8", "g8") if act8 else ("x", "r", "g"))
+    y, h = bd.gated_scan(c["x"], c["r"], c["g"], c["lam"], bd.gated_dims(E, dtype), B, L, h0=c["h0"],
+                         lengths=lengths_tensor(d, L))
+    check_forward(d, y, h, B, L, False)
