@@ -228,3 +228,23 @@ def test_every_choice_of_clusters(B, L, E, lens, dtype, act8):
     y, h = bd.gated_scan(c["x"], c["r"], c["g"], c["lam"], bd.gated_dims(E, dtype), B, L, h0=c["h0"],
                          lengths=lengths_tensor(d, L))
     check_forward(d, y, h, B, L, False)
+
+
+@pytest.mark.parametrize("B,L,E", [(2, 1, 64), (2, 100, 70), (2, 700, 96), (1, 2100, 64), (3, 3, 40)])
+def test_state_gradient_over_the_final_one(B, L, E):
+    """dh0 = dh_last in blocks of both shapes, in a cluster and with a sequence of no positions (the C interface; the
+    binding allocates dh0)."""
+    for lens in (None, [0] + [L] * (B - 1)):
+        d = make(B, L, E, FP32, seed=49, lens=lens)
+        c = dev(d)
+        lib, dims, lt = bd.load(), bd.gated_dims(E, FP32), lengths_tensor(d, L)
+        _, _, ck, want = train(d, c, B, L, E, FP32, False, False)
+        dh = c["dh_last"].clone()
+        gi = bd.GatedIn(*(c[k].data_ptr() for k in ("x", "r", "g")), E, E, E, c["lam"].data_ptr(), None)
+        got = {k: torch.empty_like(want[k]) for k in ("dx", "dr", "dg", "dlam")}
+        gr = bd.GatedGrads(*(got[k].data_ptr() for k in ("dx", "dr", "dg")), E, E, E, got["dlam"].data_ptr(), dh.data_ptr())
+        ws = torch.empty(bd.gated_scan_backward_workspace_size(dims, B, L), dtype=torch.uint8, device="cuda")
+        assert lib.r2l_gated_scan_backward(gi, c["dy"].data_ptr(), E, dh.data_ptr(), gr, dims, B, L,
+                                           None if lt is None else lt.data_ptr(), ck.data_ptr(), ck.numel(), ws.data_ptr(),
+                                           ws.numel(), torch.cuda.current_stream().cuda_stream) == 0
+        assert torch.equal(dh, want["dh0"]) and all(torch.equal(got[k], want[k]) for k in got)
