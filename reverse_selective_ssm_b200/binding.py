@@ -448,7 +448,10 @@ def _int(v: int) -> int:
 
 
 def _positions(B: int, L: int) -> int:
-    return _int(B) * _int(L)
+    M = B * L
+    if not 0 <= M < 1 << 31:         # else each is below 2^31, or one is 0, which the library refuses
+        return _int(B) * _int(L)
+    return M
 
 
 @contextlib.contextmanager
@@ -544,7 +547,7 @@ def _gated_forward(x, r, g, lam, dims, B, L, h0, lengths, checkpoint, y, h_last,
         py, ldy = _rows(y, B * L, E, x.dtype, dev, "y")
         ph = _vec(h_last, (B, E), dev, "h_last")
         pl = _vec(lengths, (B,), dev, "lengths", torch.int32)
-        ps = _status(status, dev)
+        ps = None if status is None else _status(status, dev)
         if not train:
             return lib.r2l_gated_scan(gi, py, ldy, ph, dims, B, L, pl, ps, st)
         if checkpoint is None:
