@@ -437,9 +437,10 @@ R2L_API r2l_status r2l_gated_scan(const r2l_gated_in *in, void *y, int ldy, floa
  * input.  Without R2L_FLAG_ACT8 it holds the state that enters every
  * R2L_GATED_TILE-th position of the scan order (fp32, 1/16 byte per position
  * and channel); with it also x, r and g as r2l_act8_pack packs them (3 + 3/64
- * bytes per position and channel), after the same states; an r or g beyond
- * ±256, infinite or finite, is kept as ±256, which closes or opens that gate
- * just the same.  Channels are rounded up to R2L_ACT8_GROUP.                 */
+ * bytes per position and channel), after the same states; but an r or g counts
+ * for its scale up to ±256 only, and what lies beyond, infinite or finite, is
+ * kept as a value from ±256 to ±448, which closes or opens that gate just the
+ * same.  Channels are rounded up to R2L_ACT8_GROUP.                          */
 R2L_API size_t r2l_gated_scan_checkpoint_size(const r2l_dims *dims, int B, int L);
 
 /* r2l_gated_scan for training: also writes `checkpoint`

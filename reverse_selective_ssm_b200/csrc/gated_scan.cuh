@@ -384,17 +384,21 @@ __device__ __forceinline__ void store_if(float* at, int j, int rows, float v) {
                : "memory");
 }
 
-// What an 8-bit checkpoint holds of values far out.  A gate beyond ±256 is kept
-// as ±256: its sigmoid is 0 or 1 in fp32 from ±104 on, and a mask of the type's
-// lowest value, or an infinity, leaves its scale's other channels the steps of
-// a group that reaches 256.  x as in act8::storable.
-constexpr float GATE_MAX = 256.0f;
-constexpr uint32_t GATE_MAX_BITS = 0x43800000u;     // its bits
-__device__ __forceinline__ float storable(float v, bool gate) {
-  return !gate ? act8::storable(v) : fabsf(v) > GATE_MAX ? copysignf(GATE_MAX, v) : v;
-}
+// What an 8-bit checkpoint holds of values far out.  A gate counts for its scale
+// up to ±256, and e4m3's conversion holds what lies beyond as ±448 at most: its
+// sigmoid is 0 or 1 in fp32 from ±104 on, and a mask of the type's lowest value,
+// or an infinity, leaves its scale's other channels the steps of a group that
+// reaches 256.  x as in act8::storable.
+constexpr uint32_t GATE_MAX_BITS = 0x43800000u;     // of 256
+__device__ __forceinline__ float storable(float v, bool gate) { return gate ? v : act8::storable(v); }
 __device__ __forceinline__ float2 storable(float2 v, bool gate) {
   return make_float2(storable(v.x, gate), storable(v.y, gate));
+}
+
+// |v| as bits, 0 for a NaN: an x that is stored has no infinities, and a gate's count like 256.
+__device__ __forceinline__ uint32_t counted(float v) {
+  const uint32_t bits = __float_as_uint(v) & 0x7fffffffu;
+  return bits <= 0x7f800000u ? bits : 0u;
 }
 
 // A lane's two channels at `at`, where j < rows (as a predicate, not a branch).
@@ -649,13 +653,15 @@ __global__ void __launch_bounds__(WARPS * 32, 16 / WARPS)
                     0xffffffffu, !ANY ? lane_abs_max(in + i * ARRAY + j * Lay::ROW, lane) : abs_max(value(i, j)));
               if (lane == i * ROWS + j) top = m;
             }
-          const bool odd = __any_sync(0xffffffffu, top >= (lane < ROWS ? act8::SPECIAL : GATE_MAX_BITS + 1));
+          const uint32_t most = lane < ROWS ? 0xffffffffu : GATE_MAX_BITS;
+          if (top <= 0x7f800000u) top = min(top, most);
+          const bool odd = __any_sync(0xffffffffu, top >= act8::SPECIAL);     // a NaN, or an x far out
           if (odd) {
 #pragma unroll 1
             for (int c = 0; c < 3 * ROWS; ++c) {
               const float2 v = storable(value(c / ROWS, c % ROWS), c >= ROWS);
-              const uint32_t m = __reduce_max_sync(0xffffffffu, max(act8::finite_abs_bits(v.x), act8::finite_abs_bits(v.y)));
-              if (lane == c) top = m;
+              const uint32_t m = __reduce_max_sync(0xffffffffu, max(counted(v.x), counted(v.y)));
+              if (lane == c) top = min(m, most);
             }
           }
           const uint32_t byte = act8::scale_byte(top);

@@ -248,3 +248,34 @@ def test_state_gradient_over_the_final_one(B, L, E):
                                            None if lt is None else lt.data_ptr(), ck.data_ptr(), ck.numel(), ws.data_ptr(),
                                            ws.numel(), torch.cuda.current_stream().cuda_stream) == 0
         assert torch.equal(dh, want["dh0"]) and all(torch.equal(got[k], want[k]) for k in got)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP32], ids=["bf16", "fp32"])
+@pytest.mark.parametrize("E", [64, 67])
+def test_nan_beside_gates_far_out_in_8_bits(E, dtype):
+    """A NaN in x, r or g among masked gates and far values of the same scales stays in its channel."""
+    B, L = 1, 100
+    d = make(B, L, E, dtype, seed=51)
+    low, nan = torch.finfo(dtype).min, float("nan")
+    d["x"][40, 5] = d["r"][41, 9] = d["g"][42, 13] = nan
+    d["r"][41, 10], d["r"][41, 11], d["g"][42, 14], d["g"][42, 15] = low, INF, -1e9, -INF
+    d["r"][43, 20], d["x"][44, 21] = -INF, 1e30
+    _, _, _, out = train(d, dev(d), B, L, E, dtype, True, True)
+    clean = dict(d)
+    for k in ("x", "r", "g"):
+        clean[k] = d[k].clone().nan_to_num(nan=0.0, posinf=INF, neginf=-INF)
+    keep = torch.ones(E, dtype=torch.bool)
+    keep[[5, 9, 13]] = False
+    for k, v in out.items():
+        v = v.cpu()
+        assert bool(torch.isnan(v[..., ~keep]).any()) and not bool(torch.isnan(v[..., keep]).any()), k
+    for k in ("x", "r", "g"):
+        v = S.to_f64(clean[k])
+        held = O.act8_values(v if k == "x" else np.clip(v, -256.0, 256.0))
+        clean[k + "8"] = torch.from_numpy(held if k == "x" else np.where(np.abs(v) >= 256.0, np.copysign(np.inf, v), held))
+    # the NaN channels aside, all is as if they held zeros there (a zero does not count for a scale either)
+    want = {k: v.cpu().clone() for k, v in out.items()}
+    _, _, _, zeros = train(clean, dev(clean), B, L, E, dtype, True, True)
+    for k in want:
+        assert torch.equal(want[k][..., keep], zeros[k].cpu()[..., keep]), k
+    check_backward(clean, zeros, B, L, True, ("x8", "r8", "g8"))
