@@ -22,7 +22,7 @@ namespace {
 // fp32 rows are nearer to what memory gives, so fewer clusters of 4 pay (64 blocks
 // of 600 positions: single 9.4 us, clusters of 4 11.5), and with their 8-bit copies
 // clusters of 8 leave shared memory for one block an SM (one sequence of 2048 x
-// 2048, 32 blocks: 49.9 us, clusters of 4 33.1).
+// 2048, 32 blocks: 47.1 us, clusters of 4 31.5).
 Split forward_split(int B, int E, int L, int mode, int size, bool lengths) {
   const long long jobs64 = (long long)B * ((E - 1) / 64 + 1), jobs32 = (long long)B * ((E - 1) / 32 + 1);
   if (L < 512 || (L < 1024 && jobs64 > 592)) return {1, 4};

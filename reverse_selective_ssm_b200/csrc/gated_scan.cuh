@@ -522,10 +522,10 @@ constexpr int ROWS = 8;      // consecutive rows of a thread
 
 // Whether rows that start anywhere come in whole pieces.  The 8-bit forward in
 // fp32 has no registers to spare: in blocks of 8 warps it spills with them and
-// takes 29.1 us of 5 ragged x 777 x 515 (by elements 26.6), 68.5 of 16 x 1000 x
-// 515 (60.7) and 128 of 8 x 2000 x 1037 (115).  In blocks of 4 warps pieces are
-// ahead all the same (61 x 512 x 1037: 181 us and 189), and so they are in bf16
-// (8 x 2000 x 1037: 116 us and 125).
+// takes 25.8 us of 5 ragged x 777 x 515 (by elements 23.9), 65.6 of 16 x 1000 x
+// 515 (58.1) and 122 of 8 x 2000 x 1037 (111).  In blocks of 4 warps pieces are
+// ahead all the same (61 x 512 x 1037: 180 us and 186), and so they are in bf16
+// (8 x 2000 x 1037: 101 us and 118).
 template <typename T, bool VEC, int MODE, int WARPS>
 constexpr bool WHOLE_PIECES = !VEC && !(MODE == 2 && sizeof(T) == 4 && WARPS == 8);
 
